@@ -249,7 +249,7 @@ def _plain_step(s):
         v = root * root
     m = m * BETA1 + x * (1 - BETA1)
     v = v * BETA2 + (x * x) * (1 - BETA2)
-    root = v.sqrt()
+    root = v.double().sqrt().float()     # rounded to the nearest: what is stored of it depends on its last bit
     a = (LR * s["ls"] * s["wd"]).float()
     b = (LR * s["ls"] * (1 / (1 - BETA1 ** t))).float()
     d = root * (1 / math.sqrt(1 - BETA2 ** t)) + EPS
