@@ -165,8 +165,8 @@ def prepare(case, seed):
         zero(m.view(-1))
         zero(v.view(-1))
         if case["bits"] == 8:
-            s["m"], s["m_scale"] = _encode_near(m)
-            s["s"], s["s_scale"] = _encode_near(v.sqrt())
+            s["m8"], s["m_scale"] = _encode_near(m)
+            s["s8"], s["s_scale"] = _encode_near(v.sqrt())
         else:
             s["m"], s["v"] = m, v
     if own:
@@ -244,8 +244,8 @@ def _plain_step(s):
     if "v" in s:
         m, v = s["m"], s["v"]
     else:
-        m = s["m"].float() * s["m_scale"]
-        root = s["s"].float() * s["s_scale"]
+        m = s["m8"].float() * s["m_scale"]
+        root = s["s8"].float() * s["s_scale"]
         v = root * root
     m = m * BETA1 + x * (1 - BETA1)
     v = v * BETA2 + (x * x) * (1 - BETA2)
@@ -270,8 +270,8 @@ def _plain_step(s):
         s["v"].copy_(v)
     else:
         h = _bits(s["seed"], t, s["tensor"], s["first"] + torch.arange(RUN, device=x.device))
-        s["m"], s["m_scale"] = _encode(m, h & 0xFFFF, False)
-        s["s"], s["s_scale"] = _encode(root, h >> 16, True)
+        s["m8"], s["m_scale"] = _encode(m, h & 0xFFFF, False)
+        s["s8"], s["s_scale"] = _encode(root, h >> 16, True)
     return out
 
 
@@ -288,7 +288,7 @@ def _own_step(s):
 def run(s):
     if s["op"] == "step":
         out = _own_step(s) if own else _plain_step(s)
-        for name in ("p", "rem", "m", "v", "m_scale", "s", "s_scale"):
+        for name in ("p", "rem", "m", "v", "m8", "m_scale", "s8", "s_scale"):
             if name in s:
                 out[name] = s[name].view(-1)
         return out
@@ -360,7 +360,7 @@ def exact(case, seed):
     t = STEP0 + 1
     x = g * (coef if case["clip"] else 1.0)
     if case["bits"] == 8:
-        m0, v0 = s["m"].double() * s["m_scale"].double(), (s["s"].double() * s["s_scale"].double()) ** 2
+        m0, v0 = s["m8"].double() * s["m_scale"].double(), (s["s8"].double() * s["s_scale"].double()) ** 2
     else:
         m0, v0 = s["m"].double(), s["v"].double()
     p0 = s["p"].double().view(-1, RUN)
@@ -375,8 +375,8 @@ def exact(case, seed):
     out["p"] = ((1 - lr * s["wd"]) * p0 - lr * update).reshape(-1)
     if case["bits"] == 8:
         h = _hashed(s["seed"], t, s["tensor"], s["first"] + torch.arange(RUN, device=g.device))
-        out["m"], out["m_scale"] = _stored(m, h % 65536, False)
-        out["s"], out["s_scale"] = _stored(v.sqrt(), h // 65536, True)
+        out["m8"], out["m_scale"] = _stored(m, h % 65536, False)
+        out["s8"], out["s_scale"] = _stored(v.sqrt(), h // 65536, True)
     else:
         out["m"], out["v"] = m.reshape(-1), v.reshape(-1)
     return out
