@@ -422,6 +422,153 @@ void shampoo_destroy(shampoo_t* h);
 /* Static text for a status code. */
 const char* shampoo_strerror(int status);
 
+/* ================================================== first-order operators
+ * One AdamW step over many tensors at once, with moments in 32 or in 8 bits,
+ * for what stands beside the Shampoo blocks (biases, norm gains, embeddings,
+ * heads), and the global gradient norm that both kinds of step are clipped
+ * by.  The same conventions as above, with these additions: tensors have the
+ * types that their descriptors say, any shape (contiguous; only the element
+ * count matters) and may start at any element; sizes of 0 are allowed.  The
+ * calls below other than *_bind_state allocate nothing, upload nothing and
+ * never wait, so they can be captured into a graph; replays count steps on.
+ * Calls need the device current that was current at *_bind_state
+ * (SHAMPOO_E_STATE otherwise).  Results do not depend on how the work was
+ * distributed: they are bit for bit repeatable. */
+
+typedef enum { SHAMPOO_F32 = 0, SHAMPOO_BF16 = 1, SHAMPOO_F16 = 2 } shampoo_dtype;
+
+/* ---- global gradient norm ---- */
+typedef struct shampoo_gradnorm_s shampoo_gradnorm_t; /* opaque; host memory only */
+
+typedef struct {
+    int64_t numel;
+    int32_t dtype;     /* shampoo_dtype */
+    int32_t reserved;  /* must be 0 */
+} shampoo_grad_desc;
+
+/* What shampoo_gradnorm_compute leaves on the device. */
+typedef struct {
+    float norm;          /* n = grad_scale sqrt(sum of all g^2), summed in fp64          */
+    float coef;          /* grad_scale min(1, max_norm / n): the factor of a clipped
+                            gradient; 0 when n is not finite                             */
+    int32_t nonfinite;   /* 1: n is not finite (some gradient is infinite or NaN)        */
+    int32_t reserved;
+} shampoo_clip_record;
+
+/* Plan for the gradients of n_tensors tensors.  Host only.  Errors:
+ * SHAMPOO_E_ARG (null, n_tensors < 1, numel < 0, unknown dtype, reserved not
+ * 0), SHAMPOO_E_UNSUPPORTED (numel above 2^38), SHAMPOO_E_NOMEM. */
+int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
+                            shampoo_gradnorm_t** out);
+/* Bytes of device state (tables, partial sums, the record); 256-byte aligned,
+ * alive and in place while the handle is used.  Host only. */
+int shampoo_gradnorm_state_bytes(const shampoo_gradnorm_t* h, size_t* bytes);
+/* Attach and initialise the state; waits for that.  Errors: SHAMPOO_E_ARG
+ * (null, unaligned), SHAMPOO_E_STATE (too small), SHAMPOO_E_HIP. */
+int shampoo_gradnorm_bind_state(shampoo_gradnorm_t* h, void* dev_state, size_t bytes, void* stream);
+/* The gradients' device addresses from now on (until bound again; the calls
+ * that follow on `stream` read them).  A null gradient counts as absent.
+ * outs: NULL, or for each tensor null or the fp32 tensor that
+ * shampoo_gradnorm_clip_into fills: the gradient itself where that is fp32,
+ * otherwise memory that overlaps no gradient.  Errors: SHAMPOO_E_ARG (null
+ * grads, an address not aligned to its element, an output in place of a
+ * gradient that is not fp32), SHAMPOO_E_STATE, SHAMPOO_E_HIP. */
+int shampoo_gradnorm_bind_grads(shampoo_gradnorm_t* h, const void* const* grads, float* const* outs,
+                                void* stream);
+/* Norm and clip coefficient of the bound gradients into the device record.
+ * max_norm: > 0, or infinity for no clipping.  grad_scale: a factor that the
+ * gradients are first taken to carry (1, or 1 / loss scale).  Errors:
+ * SHAMPOO_E_ARG (max_norm not > 0, grad_scale not > 0 or not finite),
+ * SHAMPOO_E_STATE, SHAMPOO_E_HIP. */
+int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad_scale, void* stream);
+/* out <- coef g, in fp32, for every bound output, by the record of the last
+ * shampoo_gradnorm_compute; 0 everywhere when the norm was not finite, so
+ * that a Shampoo step that takes these gradients adds nothing to its
+ * statistics.  Errors: SHAMPOO_E_STATE, SHAMPOO_E_HIP. */
+int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream);
+/* Device address of the record (inside the state buffer).  Host only. */
+int shampoo_gradnorm_record(const shampoo_gradnorm_t* h, const shampoo_clip_record** dev_record);
+void shampoo_gradnorm_destroy(shampoo_gradnorm_t* h);
+
+/* ---- AdamW ---- */
+typedef struct shampoo_adamw_s shampoo_adamw_t; /* opaque; host memory only */
+
+typedef struct {
+    double beta1, beta2;  /* in [0, 1)                                                   */
+    double eps;           /* > 0                                                         */
+    uint32_t seed;        /* of the rounding of 8-bit moments                            */
+    int32_t reserved;     /* must be 0                                                   */
+} shampoo_adamw_config;
+
+typedef struct {
+    int64_t numel;
+    int32_t param_type;   /* SHAMPOO_F32, or SHAMPOO_BF16: the weight is the bf16 value plus
+                             a 16-bit remainder in the state, together its fp32 value    */
+    int32_t grad_type;    /* shampoo_dtype */
+    int32_t state_bits;   /* 32: fp32 moments; 8: e4m3 codes of m and of sqrt(v) with one
+                             fp32 scale per run of 256 elements each                     */
+    int32_t reserved;     /* must be 0 */
+    double weight_decay;  /* >= 0 */
+    double lr_scale;      /* >= 0: the tensor's learning rate is lr lr_scale             */
+} shampoo_adamw_tensor;
+
+/* Byte offsets in the state buffer.  A tensor's state starts at a run of 256
+ * elements (shampoo_adamw_tensor_runs) and fills whole runs; what lies behind
+ * its last element is 0. */
+typedef struct {
+    int64_t total;                 /* bytes of the state                                */
+    int64_t off_clock;             /* int64: steps done                                 */
+    int64_t runs32, off_m, off_v;  /* fp32 moments: runs of the region, m, v            */
+    int64_t runs8, off_m8, off_s8; /* 8-bit moments: runs, codes of m and of sqrt(v)    */
+    int64_t off_m_scale, off_s_scale;  /* fp32, one per run                              */
+    int64_t runs_rem, off_rem;     /* bf16 weights: runs, int16 remainders              */
+} shampoo_adamw_layout;
+
+/* Plan for n_tensors tensors.  Host only.  Errors: SHAMPOO_E_ARG (null,
+ * n_tensors < 1, numel < 0, a beta outside [0, 1), eps not > 0 in fp32 or not
+ * finite, weight_decay or lr_scale negative or not finite, unknown types,
+ * state_bits not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16
+ * weights, numel above 2^38), SHAMPOO_E_NOMEM. */
+int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,
+                         const shampoo_adamw_tensor* tensors, shampoo_adamw_t** out);
+int shampoo_adamw_get_layout(const shampoo_adamw_t* h, shampoo_adamw_layout* out);
+/* First run of a tensor in its moments' region, and in the remainders' (-1
+ * for fp32 weights).  Host only. */
+int shampoo_adamw_tensor_runs(const shampoo_adamw_t* h, int32_t tensor, int64_t* state_run,
+                              int64_t* rem_run);
+/* Attach the state (layout.total bytes, 256-byte aligned) and initialise it:
+ * moments and remainders 0, no steps done.  Waits for that.  Errors:
+ * SHAMPOO_E_ARG, SHAMPOO_E_STATE (too small), SHAMPOO_E_HIP. */
+int shampoo_adamw_bind_state(shampoo_adamw_t* h, void* dev_state, size_t bytes, void* stream);
+/* The tensors' device addresses from now on, until bound again; params or
+ * grads may be NULL to keep those bound before.  A null gradient (none this
+ * step) leaves its tensor's weights and moments as they are.  Gradients and
+ * weights must not overlap each other.  Errors: SHAMPOO_E_ARG (both NULL, a
+ * null weight, an address not aligned to its element), SHAMPOO_E_STATE,
+ * SHAMPOO_E_HIP. */
+int shampoo_adamw_bind_tensors(shampoo_adamw_t* h, void* const* params, const void* const* grads,
+                               void* stream);
+/* Set the number of steps done (t >= 0), e.g. after restoring the moments. */
+int shampoo_adamw_set_step(shampoo_adamw_t* h, int64_t t, void* stream);
+/* One step of every bound tensor:
+ *   x = coef g;  m = beta1 m + (1 - beta1) x;  v = beta2 v + (1 - beta2) x^2
+ *   p = p - lr' (weight_decay p + (m / (1 - beta1^t)) /
+ *                (sqrt(v / (1 - beta2^t)) + eps)),      lr' = lr lr_scale
+ * t counting from 1.  lr: the learning rate, unless dev_lr is given: one fp32
+ * on the device, read when the step runs.  dev_clip: NULL (coef 1), or a
+ * record of shampoo_gradnorm_compute: coef is its coefficient, and where it
+ * says nonfinite the step leaves weights, moments and t as they are.
+ * 8-bit moments are rounded to the code below or above at random, with the
+ * probabilities that make the mean of what is stored the value itself; the
+ * random bits are a hash of (seed, t, tensor index, element).  A positive
+ * sqrt(v) is never stored as 0; a value that is not finite is stored as NaN
+ * and does not touch its run's scale.
+ * Errors: SHAMPOO_E_ARG (lr not finite, a misaligned pointer), SHAMPOO_E_STATE
+ * (state, weights or gradients not bound), SHAMPOO_E_HIP. */
+int shampoo_adamw_step(shampoo_adamw_t* h, double lr, const float* dev_lr,
+                       const shampoo_clip_record* dev_clip, void* stream);
+void shampoo_adamw_destroy(shampoo_adamw_t* h);
+
 #ifdef __cplusplus
 }
 #endif

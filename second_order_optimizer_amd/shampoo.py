@@ -75,6 +75,28 @@ class KernelTime(ctypes.Structure):
                 ("total_ms", ctypes.c_double)]
 
 
+class GradDesc(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("seed", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("param_type", ctypes.c_int32),
+                ("grad_type", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("weight_decay", ctypes.c_double),
+                ("lr_scale", ctypes.c_double)]
+
+
+class AdamWLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("total", "off_clock", "runs32", "off_m", "off_v", "runs8", "off_m8", "off_s8",
+                 "off_m_scale", "off_s_scale", "runs_rem", "off_rem")]
+
+
 # name -> (restype, argtypes); every symbol declared in include/shampoo.h
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -104,6 +126,25 @@ SIGNATURES = {
     "shampoo_profile_read": (ctypes.c_int, [_P, ctypes.POINTER(KernelTime), ctypes.c_int32,
                                             ctypes.POINTER(ctypes.c_int32)]),
     "shampoo_measure_peaks": (ctypes.c_int, [ctypes.POINTER(Peaks), _P, ctypes.c_size_t, _P]),
+    "shampoo_gradnorm_create": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(GradDesc),
+                                               ctypes.POINTER(_P)]),
+    "shampoo_gradnorm_state_bytes": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "shampoo_gradnorm_bind_state": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "shampoo_gradnorm_bind_grads": (ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P]),
+    "shampoo_gradnorm_compute": (ctypes.c_int, [_P, ctypes.c_double, ctypes.c_double, _P]),
+    "shampoo_gradnorm_clip_into": (ctypes.c_int, [_P, _P]),
+    "shampoo_gradnorm_record": (ctypes.c_int, [_P, ctypes.POINTER(_P)]),
+    "shampoo_gradnorm_destroy": (None, [_P]),
+    "shampoo_adamw_create": (ctypes.c_int, [ctypes.POINTER(AdamWConfig), ctypes.c_int32,
+                                            ctypes.POINTER(AdamWTensor), ctypes.POINTER(_P)]),
+    "shampoo_adamw_get_layout": (ctypes.c_int, [_P, ctypes.POINTER(AdamWLayout)]),
+    "shampoo_adamw_tensor_runs": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64),
+                                                 ctypes.POINTER(ctypes.c_int64)]),
+    "shampoo_adamw_bind_state": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "shampoo_adamw_bind_tensors": (ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P]),
+    "shampoo_adamw_set_step": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
+    "shampoo_adamw_step": (ctypes.c_int, [_P, ctypes.c_double, _P, _P, _P]),
+    "shampoo_adamw_destroy": (None, [_P]),
     "shampoo_destroy": (None, [_P]),
     "shampoo_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }

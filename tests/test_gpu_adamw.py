@@ -1,0 +1,657 @@
+"""The first-order operators on the GPU against the fp64 oracle: one AdamW step
+over many tensors with moments in 32 and in 8 bits, and the global gradient
+norm.  Every bound is the oracle's count of fp32 roundings along the formula."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import adamw_oracle as O
+from second_order_optimizer_amd import adamw as A
+from second_order_optimizer_amd import shampoo as S
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+GUARD = 16      # elements beside a tensor that nothing may touch
+SENTINEL = -77.0
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def guarded(values, dtype, offset):
+    """A device tensor of `values` inside a buffer of sentinels, starting
+    `offset` elements past an aligned address; and the buffer."""
+    n = values.size
+    buf = torch.full((n + 2 * GUARD + 4,), SENTINEL, dtype=dtype, device="cuda")
+    t = buf[GUARD + offset:GUARD + offset + n]
+    t.copy_(torch.from_numpy(values).to(dtype))
+    return t, buf
+
+
+def untouched(buf, offset, n):
+    b = buf.float().cpu().numpy()
+    assert np.all(b[:GUARD + offset] == SENTINEL) and np.all(b[GUARD + offset + n:] == SENTINEL)
+
+
+class Run:
+    """An AdamW handle over tensors with random weights, gradients and moments,
+    and the oracle's check of one step of it."""
+
+    def __init__(self, specs, seed, *, offset=0, beta1=0.9, beta2=0.999, eps=1e-8, t0=0, warm=True):
+        self.rng = np.random.default_rng(seed)
+        self.specs, self.offset = specs, offset
+        self.cfg = A.make_config(beta1=beta1, beta2=beta2, eps=eps, seed=seed)
+        self.opt = A.AdamW(specs, self.cfg)
+        self.types = [("f32", "bf16")[s.param_type] for s in specs]
+        self.gtypes = [("f32", "bf16", "f16")[s.grad_type] for s in specs]
+        self.sigma = [10 ** self.rng.uniform(-4, 0) for _ in specs]
+        self.params, self.grads, self.bufs = [], [], []
+        for s, dt in zip(specs, self.types):
+            w = (0.02 * self.rng.standard_normal(s.numel)).astype(np.float32)
+            t, b = guarded(w, TORCH[dt], offset)
+            self.params.append(t)
+            self.bufs.append((b, s.numel))
+        for i in range(len(specs)):
+            t, b = guarded(self.draw(i), TORCH[self.gtypes[i]], offset)
+            self.grads.append(t)
+            self.bufs.append((b, specs[i].numel))
+        if warm:
+            self.warm()
+        self.opt.set_step(t0)
+        self.t = t0
+        self.opt.bind(self.params, self.grads)
+
+    def draw(self, i):
+        return (self.sigma[i] * self.rng.standard_normal(self.specs[i].numel)).astype(np.float32)
+
+    def place(self, i):
+        st, rm = ctypes.c_int64(), ctypes.c_int64()
+        assert S.lib().shampoo_adamw_tensor_runs(self.opt.h, i, ctypes.byref(st), ctypes.byref(rm)) == 0
+        return st.value, rm.value
+
+    def parts(self, i):
+        """Views of tensor i's state: elements, and its runs' scales."""
+        s, held = self.specs[i], self.opt.state_tensors()
+        st, rm = self.place(i)
+        n, runs = s.numel, -(-s.numel // 256)
+        cut = lambda x, r: x[r * 256:r * 256 + n]
+        out = {}
+        if n == 0:
+            return out
+        if s.state_bits == 32:
+            out.update(m=cut(held["m"], st), v=cut(held["v"], st))
+        else:
+            out.update(m8=cut(held["m8"].view(torch.uint8), st), s8=cut(held["s8"].view(torch.uint8), st),
+                       m_scale=held["m_scale"][st:st + runs], s_scale=held["s_scale"][st:st + runs])
+        if rm >= 0:
+            out["rem"] = cut(held["rem"], rm)
+        return out
+
+    def warm(self):
+        for i, s in enumerate(self.specs):
+            q = self.parts(i)
+            n, runs = s.numel, -(-s.numel // 256)
+            if "m" in q:
+                q["m"].copy_(torch.from_numpy(0.3 * self.draw(i)))
+                q["v"].copy_(torch.from_numpy(self.draw(i) ** 2))
+            elif n:
+                q["m8"].copy_(torch.from_numpy(self.codes(n, True)))
+                q["s8"].copy_(torch.from_numpy(self.codes(n, False)))
+                for k in ("m_scale", "s_scale"):
+                    x = self.sigma[i] / 448 * (0.5 + self.rng.random(runs))
+                    q[k].copy_(torch.from_numpy(x.astype(np.float32)))
+            if "rem" in q:
+                q["rem"].copy_(torch.from_numpy(self.rng.integers(-32768, 32768, n).astype(np.int16)))
+
+    def codes(self, n, signed):
+        c = self.rng.integers(0, 127, n)
+        if signed:
+            c |= 128 * self.rng.integers(0, 2, n)
+        return c.astype(np.uint8)
+
+    def read(self):
+        """Weights (as fp32 values), moments and their errors, in fp64."""
+        got = []
+        for i, s in enumerate(self.specs):
+            q = {k: x.cpu().numpy().copy() for k, x in self.parts(i).items()}
+            w = self.params[i].detach().cpu()
+            if "rem" in q:
+                q["p"] = O.bf16_join(w.view(torch.int16).numpy().view(np.uint16), q["rem"]).astype(np.float64)
+            else:
+                q["p"] = w.double().numpy()
+            if "m8" in q:
+                n = s.numel
+                q["m"] = O.decode(q["m8"]) * np.repeat(q["m_scale"].astype(np.float64), 256)[:n]
+                root = O.decode(q["s8"]) * np.repeat(q["s_scale"].astype(np.float64), 256)[:n]
+                q["v"] = root * root
+                q["m_err"], q["v_err"] = O.U * np.abs(q["m"]), 3 * O.U * q["v"]
+            elif s.numel:
+                q["m"], q["v"] = q["m"].astype(np.float64), q["v"].astype(np.float64)
+                q["m_err"] = q["v_err"] = 0.0
+            else:
+                q["m"] = q["v"] = np.zeros(0)
+                q["m_err"] = q["v_err"] = 0.0
+            q["g"] = np64(self.grads[i]) if self.grads[i] is not None else None
+            got.append(q)
+        return got
+
+    def hyper(self, i, lr):
+        s, c = self.specs[i], self.cfg
+        return O.Hyper(c.beta1, c.beta2, c.eps, lr, s.weight_decay, s.lr_scale)
+
+    def check(self, before, lr, coef=1.0):
+        """The state now is one step on from `before`."""
+        self.t += 1
+        assert int(self.opt.t) == self.t
+        after = self.read()
+        for i, (a, b) in enumerate(zip(before, after)):
+            s = self.specs[i]
+            if s.numel == 0:
+                continue
+            # eps and the scalars reach the kernel as fp32: within U of these
+            p, m, root, v, pe, me, re, ve = O.step(a["p"], a["g"], a["m"], a["v"], self.t,
+                                                   self.hyper(i, lr), coef, a["m_err"], a["v_err"])
+            assert np.all(np.abs(b["p"] - p) <= pe), (i, np.max(np.abs(b["p"] - p) / pe))
+            if s.state_bits == 32:
+                assert np.all(np.abs(b["m"] - m) <= me), i
+                assert np.all(np.abs(b["v"] - v) <= ve), i
+                continue
+            rm, rs = O.random_bits(self.cfg.seed, self.t, i, np.arange(s.numel))
+            for x, xe, code, scale, r, pos in ((m, me, "m8", "m_scale", rm, False),
+                                               (root, re, "s8", "s_scale", rs, True)):
+                want = O.run_scales(x)
+                top = np.maximum.reduceat(xe, np.arange(0, s.numel, 256))
+                assert np.all(np.abs(b[scale] - want) <= top / 448 + 3 * O.U * want), (i, scale)
+                lo, hi = O.store_range(x, xe, want, r, pos)
+                z = O.decode(b[code])
+                assert np.all((np.abs(z) >= lo) & (np.abs(z) <= hi)), (i, code)
+                sure = (lo > 0) & (np.abs(x) > xe)
+                assert np.all((np.sign(z) == np.sign(x))[sure])
+                if pos:
+                    assert np.all(z[root > re] > 0)
+
+    def rest_untouched(self):
+        for b, n in self.bufs:
+            untouched(b, self.offset, n)
+        for i, s in enumerate(self.specs):      # state behind the last element stays 0
+            if s.numel % 256 == 0:
+                continue
+            st, rm = self.place(i)
+            held = self.opt.state_tensors()
+            names = [("m", st), ("v", st)] if s.state_bits == 32 else [("m8", st), ("s8", st)]
+            for name, r in names + ([("rem", rm)] if rm >= 0 else []):
+                x = held[name].view(torch.uint8) if "8" in name else held[name]
+                gap = x[r * 256 + s.numel:(r + -(-s.numel // 256)) * 256]
+                assert not bool(gap.any()), (i, name)
+
+
+SIZES = [1, 2, 3, 5, 63, 255, 256, 257, 0, 511, 512, 513, 1000, 2047, 4097, 70001]
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,grad", [("f32", "f32"), ("f32", "bf16"), ("f32", "f16"),
+                                        ("bf16", "bf16"), ("bf16", "f32"), ("bf16", "f16")])
+def test_step(param, grad, bits, offset):
+    rng = np.random.default_rng(offset)
+    specs = [A.tensor(n, param=param, grad=grad, state_bits=bits,
+                      weight_decay=float(rng.choice([0.0, 0.1])), lr_scale=float(rng.choice([1.0, 0.5])))
+             for n in SIZES]
+    run = Run(specs, 11 + offset, offset=offset, t0=offset * 40)
+    for lr in (1e-3, 3e-4, 0.0):
+        before = run.read()
+        run.opt.step(lr)
+        run.check(before, lr)
+        for i, g in enumerate(run.grads):
+            g.copy_(torch.from_numpy(run.draw(i)))
+    run.rest_untouched()
+
+
+def test_first_steps_from_nothing():
+    """From zero moments, with t from 1: 8-bit runs whose values are all zero,
+    and runs where only some gradients are not."""
+    specs = [A.tensor(n, state_bits=b) for n in (300, 1024) for b in (32, 8)]
+    run = Run(specs, 5, warm=False)
+    for k in range(4):
+        for i, g in enumerate(run.grads):
+            x = run.draw(i)
+            x[k::3] = 0.0
+            x[:256 if k == 0 else 0] = 0.0
+            g.copy_(torch.from_numpy(x))
+        before = run.read()
+        run.opt.step(1e-2)
+        run.check(before, 1e-2)
+
+
+@pytest.mark.parametrize("beta1,beta2,eps,t0", [(0.0, 0.0, 1e-8, 0), (0.9, 0.95, 1e-6, 3), (0.99, 0.9999, 1e-15, 100000)])
+def test_hyperparameters(beta1, beta2, eps, t0):
+    specs = [A.tensor(5000, state_bits=b, weight_decay=0.01) for b in (32, 8)]
+    run = Run(specs, 3, beta1=beta1, beta2=beta2, eps=eps, t0=t0)
+    for _ in range(3):
+        before = run.read()
+        run.opt.step(1e-3)
+        run.check(before, 1e-3)
+
+
+@pytest.mark.parametrize("exponent", [-30, -20, -12, 12])
+def test_range_of_gradients(exponent):
+    """Gradients whose squares leave the normal range of fp32 on the low side,
+    and large ones."""
+    specs = [A.tensor(2000, state_bits=b) for b in (32, 8)]
+    run = Run(specs, 9, warm=False, eps=1e-20 if exponent < 0 else 1e-8)
+    for i, g in enumerate(run.grads):
+        g.copy_(torch.from_numpy((run.rng.standard_normal(2000) * 10.0 ** exponent).astype(np.float32)))
+    for _ in range(2):
+        before = run.read()
+        run.opt.step(1e-3)
+        run.check(before, 1e-3)
+
+
+def test_many_tensors_of_mixed_kinds():
+    """More tensors than one launch of the pointer kernel carries, every kind of
+    them in one plan, some without a gradient."""
+    rng = np.random.default_rng(2)
+    specs = []
+    for _ in range(450):
+        param = ("f32", "bf16")[rng.integers(2)]
+        specs.append(A.tensor(int(rng.integers(0, 900)), param=param, grad=("f32", "bf16", "f16")[rng.integers(3)],
+                              state_bits=int(rng.choice([8, 32])), weight_decay=float(rng.choice([0, 0.1]))))
+    run = Run(specs, 21, offset=1)
+    absent = set(range(0, 450, 7))
+    grads = [None if i in absent else g for i, g in enumerate(run.grads)]
+    run.opt.bind(grads=grads)
+    before = run.read()
+    run.opt.step(1e-3)
+    after = run.read()
+    for i in absent:
+        for k in ("p", "m", "v", "rem", "m8", "s8", "m_scale", "s_scale"):
+            if k in before[i]:
+                assert np.array_equal(before[i][k], after[i][k]), (i, k)
+    run.opt.bind(grads=run.grads)      # and all of them again
+    run.t += 1
+    before = after
+    run.opt.step(1e-3)
+    run.check(before, 1e-3)
+    run.rest_untouched()
+
+
+def test_bf16_weights_are_the_fp32_ones():
+    """bf16 weights with their remainder follow fp32 weights bit for bit."""
+    n = 3001
+    w = np.random.default_rng(1).standard_normal(n).astype(np.float32)
+    hi, rem = O.bf16_split(w)
+    p32 = torch.from_numpy(w).cuda()
+    p16 = torch.from_numpy(hi.view(np.int16)).cuda().view(torch.bfloat16)
+    a = A.AdamW([A.tensor(n, weight_decay=0.1)])
+    b = A.AdamW([A.tensor(n, param="bf16", grad="f32", weight_decay=0.1)])
+    b.state_tensors()["rem"][:n].copy_(torch.from_numpy(rem))
+    g = torch.empty(n, device="cuda")
+    a.bind([p32], [g])
+    b.bind([p16], [g])
+    for k in range(30):
+        g.normal_(0, 10.0 ** (k % 5 - 3))
+        a.step(1e-3)
+        b.step(1e-3)
+    got = O.bf16_join(p16.view(torch.int16).cpu().numpy().view(np.uint16),
+                      b.state_tensors()["rem"][:n].cpu().numpy())
+    assert np.array_equal(got.view(np.uint32), p32.cpu().numpy().view(np.uint32))
+
+
+def test_not_finite_gradients_stay_where_they_are():
+    """Without a clip, an infinite or NaN gradient spoils its own element, not
+    its run."""
+    n = 1000
+    bad = {3: np.inf, 300: -np.inf, 301: np.nan, 999: np.nan}
+    rest = np.setdiff1d(np.arange(n), list(bad))
+    run = Run([A.tensor(n, state_bits=b) for b in (32, 8)], 4)
+    for i, g in enumerate(run.grads):
+        x = run.draw(i)
+        x[list(bad)] = 0.0
+        g.copy_(torch.from_numpy(x))
+    twin = Run([A.tensor(n, state_bits=b) for b in (32, 8)], 4)
+    for x, y in zip(run.grads, twin.grads):
+        y.copy_(x)
+    for g in run.grads:
+        for k, v in bad.items():
+            g[k] = v
+    run.opt.step(1e-3)
+    twin.opt.step(1e-3)
+    a, b = run.read(), twin.read()
+    for x, y in zip(a, b):
+        assert np.array_equal(x["p"][rest], y["p"][rest])
+        for k in ("m8", "s8", "m_scale", "s_scale"):
+            if k in x and x[k].size == n:
+                assert np.array_equal(x[k][rest], y[k][rest])
+    assert np.array_equal(a[1]["s_scale"][1:3], b[1]["s_scale"][1:3])
+    for k in bad:
+        assert a[1]["s8"][k] == 127 and a[1]["m8"][k] & 127 == 127
+
+
+def test_skips_a_step_that_is_not_finite():
+    run = Run([A.tensor(3000, state_bits=b, param=p, grad="bf16") for b in (32, 8) for p in ("f32", "bf16")], 6)
+    norm = A.GradNorm([(3000, "bf16")] * 4)
+    norm.bind(run.grads)
+    run.grads[2][1234] = float("inf")
+    before = run.read()
+    norm.compute(1.0)
+    run.opt.step(1e-3, clip=norm)
+    after = run.read()
+    assert int(run.opt.t) == 0 and int(norm.nonfinite) == 1 and float(norm.record[1]) == 0.0
+    for a, b in zip(before, after):
+        for k in a:
+            assert np.array_equal(a[k], b[k], equal_nan=True), k
+    run.grads[2][1234] = 1.0
+    before = run.read()
+    norm.compute(1.0)
+    run.opt.step(1e-3, clip=norm)
+    run.check(before, 1e-3, float(norm.record[1]))
+
+
+def test_rounding_is_fair():
+    """The mean of what is stored is the value: over the 2^16 elements of equal
+    moments, within 6 standard deviations of a fair choice between the two
+    codes next to it."""
+    n = 1 << 16
+    opt = A.AdamW([A.tensor(n, state_bits=8)], A.make_config(beta1=0.5, beta2=0.5, seed=3))
+    g = torch.full((n,), 0.37, device="cuda")
+    g[::256] = 1.0           # sets each run's scale
+    p = torch.zeros(n, device="cuda")
+    opt.bind([p], [g])
+    opt.step(1e-3)
+    held = opt.state_tensors()
+    keep = np.arange(n) % 256 != 0
+    for name, scale, x in (("m8", "m_scale", 0.5 * 0.37), ("s8", "s_scale", np.sqrt(0.5) * 0.37)):
+        s = float(held[scale][0])
+        z = O.decode(held[name].view(torch.uint8).cpu().numpy())[keep]
+        y = np.float64(np.float32(x)) / s
+        lo, hi = O.store(np.array([y, y]), np.array([0.0, 65535.0]), False)
+        assert set(np.unique(z)) == {lo, hi}
+        share = (y - lo) / (hi - lo)
+        # fp32 places y within 8 U of itself, the hash resolves 2^-16 of a code
+        slack = 8 * O.U * y + (hi - lo) * 2.0 ** -16
+        assert abs(z.mean() - y) <= 6 * (hi - lo) * np.sqrt(share * (1 - share) / keep.sum()) + slack
+
+
+def test_small_roots_are_never_zero():
+    n = 512
+    opt = A.AdamW([A.tensor(n, state_bits=8)])
+    g = torch.zeros(n, device="cuda")
+    g[0], g[1:256] = 1e3, 1e-9
+    p = torch.zeros(n, device="cuda")
+    opt.bind([p], [g])
+    for _ in range(3):
+        opt.step(1e-3)
+    s = opt.state_tensors()["s8"].view(torch.uint8)
+    assert bool((s[:256] > 0).all()) and not bool(s[256:].any())
+    assert bool(torch.isfinite(p).all()) and float(p[1:].abs().max()) <= 3 * 1e-3
+
+
+def test_repeats_bit_for_bit_and_by_tensor_alignment():
+    """The same step twice, from buffers of another alignment, gives the same
+    bits."""
+    specs = [A.tensor(n, param="bf16", state_bits=8) for n in (100, 5000, 70000)]
+    got = []
+    for offset in (0, 0, 3):
+        run = Run(specs, 8, offset=offset)
+        for _ in range(3):
+            run.opt.step(1e-3)
+        got.append(run.read())
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            for k in ("p", "rem", "m8", "s8", "m_scale", "s_scale"):
+                assert np.array_equal(a[k], b[k]), k
+
+
+def test_learning_rate_on_the_device():
+    run = Run([A.tensor(1000, state_bits=b) for b in (32, 8)], 2)
+    lr = torch.tensor([1e-3], device="cuda")
+    for x in (1e-3, 5e-4):
+        lr.fill_(x)
+        before = run.read()
+        run.opt.step(lr)
+        run.check(before, float(np.float32(x)))
+
+
+def test_captured_and_replayed():
+    """Norm and step in a graph: every replay is the eager step, with eager work
+    of the same handle, new gradients, another learning rate, and a gradient
+    that is not finite between replays."""
+    sizes = (700, 5000, 40000)
+    make = lambda: Run([A.tensor(n, param="bf16", grad="bf16", state_bits=b, weight_decay=0.1)
+                        for n in sizes for b in (32, 8)], 13)
+    eager, graph = make(), make()
+    norms = [A.GradNorm([(s.numel, "bf16") for s in r.specs]) for r in (eager, graph)]
+    lrs = [torch.tensor([1e-3], device="cuda") for _ in range(2)]
+
+    def go(k):
+        (eager, graph)[k].opt.bind((eager, graph)[k].params, (eager, graph)[k].grads)
+        norms[k].bind((eager, graph)[k].grads)
+        norms[k].compute(1.0)
+        (eager, graph)[k].opt.step(lrs[k], clip=norms[k])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go(1)
+    go(0)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go(1)
+    for k in range(6):
+        for i in range(len(eager.specs)):
+            x = torch.from_numpy(eager.draw(i)).to(torch.bfloat16).cuda()
+            if k == 3 and i == 2:
+                x[17] = float("nan")
+            eager.grads[i].copy_(x)
+            graph.grads[i].copy_(x)
+        for lr in lrs:
+            lr.fill_(1e-3 / (k + 1))
+        go(0)
+        g.replay()
+        if k == 2:
+            torch.cuda.synchronize()
+            go(0)
+            go(1)
+        torch.cuda.synchronize()
+        assert int(eager.opt.t) == int(graph.opt.t)
+        assert torch.equal(norms[0].record, norms[1].record) or k == 3
+        for a, b in zip(eager.read(), graph.read()):
+            for key in a:
+                assert np.array_equal(a[key], b[key], equal_nan=True), (k, key)
+
+
+def test_another_stream():
+    a, b = Run([A.tensor(50000, state_bits=8)], 1), Run([A.tensor(50000, state_bits=8)], 1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            a.opt.step(1e-3)
+    for _ in range(3):
+        b.opt.step(1e-3)
+    torch.cuda.synchronize()
+    assert np.array_equal(a.read()[0]["p"], b.read()[0]["p"])
+
+
+def test_more_than_2_to_32_elements():
+    """Offsets and the hash past 32 bits: head, middle and tail of one tensor."""
+    n = (1 << 32) + 700
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    opt = A.AdamW([A.tensor(n, param="bf16", state_bits=8)], A.make_config(seed=5))
+    rng = np.random.default_rng(0)
+    spots = [0, 1 << 31, (1 << 32) - 256, 1 << 32, n - 700 % 256]
+    for s in spots:
+        k = min(256, n - s)
+        g[s:s + k] = torch.from_numpy(rng.standard_normal(k)).to("cuda", torch.bfloat16)
+    opt.bind([p], [g])
+    opt.step(1e-3)
+    held = opt.state_tensors()
+    assert int(torch.count_nonzero(p)) == sum(min(256, n - s) for s in spots)
+    for s in spots:
+        k = min(256, n - s)
+        gg = np64(g[s:s + k])
+        m, root = 0.1 * gg, np.sqrt(0.001) * np.abs(gg)
+        rm, rs = O.random_bits(5, 1, 0, s + np.arange(k))
+        for x, code, r, pos in ((m, "m8", rm, False), (root, "s8", rs, True)):
+            lo, hi = O.store_range(x, 8 * O.U * np.abs(x), O.run_scales(x), r, pos)
+            z = np.abs(O.decode(held[code].view(torch.uint8)[s:s + k].cpu().numpy()))
+            assert np.all((z >= lo) & (z <= hi)), (s, code)
+    del p, g, opt, held
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------ gradient norm
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("scale,grad_scale", [(1e-3, 1.0), (1.0, 0.5), (1e3, 2.0 ** -10)])
+def test_norm(offset, scale, grad_scale):
+    rng = np.random.default_rng(7)
+    kinds = ("f32", "bf16", "f16")
+    sizes = SIZES + [2048, 2049, 123457]
+    grads, bufs, want = [], [], []
+    for i, n in enumerate(sizes):
+        t, b = guarded((scale * rng.standard_normal(n)).astype(np.float32), TORCH[kinds[i % 3]], offset)
+        grads.append(t)
+        bufs.append((b, n))
+        want.append(np64(t))
+    outs, obufs = [], []
+    for n in sizes:
+        t, b = guarded(np.zeros(n, np.float32), torch.float32, 3 - offset)
+        outs.append(t)
+        obufs.append((b, n))
+    norm = A.GradNorm([(n, kinds[i % 3]) for i, n in enumerate(sizes)])
+    norm.bind(grads, outs)
+    n64, c64 = O.norm(want, 1.0, grad_scale)
+    norm.compute(1.0, grad_scale)
+    norm.clip_into()
+    got = np64(norm.record)
+    # fp64 sums: 2^-53 a term at most, then one rounding to fp32
+    assert abs(got[0] - n64) <= 2 * O.U * n64 and abs(got[1] - c64) <= 2 * O.U * c64
+    for o, w in zip(outs, want):
+        assert np.all(np.abs(np64(o) - c64 * w) <= 4 * O.U * np.abs(c64 * w) + O.TINY)
+    for b, n in bufs:
+        untouched(b, offset, n)
+    for b, n in obufs:
+        untouched(b, 3 - offset, n)
+    first = norm.record.clone()
+    norm.compute(1.0, grad_scale)
+    assert torch.equal(first, norm.record)
+
+
+def test_norm_clips_in_place_and_leaves_absent_ones():
+    rng = np.random.default_rng(3)
+    a, b, c = (torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda() for n in (5000, 300, 40))
+    keep = [x.clone() for x in (a, b, c)]
+    norm = A.GradNorm([(5000, "f32"), (300, "f32"), (40, "f32"), (9, "bf16")])
+    norm.bind([a, b, c, None], [a, None, c, None])
+    norm.compute(1.0)
+    n64, c64 = O.norm([np64(x) for x in keep], 1.0)
+    norm.clip_into()
+    assert abs(float(norm.record[0]) - n64) <= 2 * O.U * n64
+    assert np.allclose(np64(a), c64 * np64(keep[0]), rtol=4 * O.U, atol=0)
+    assert torch.equal(b, keep[1])
+    assert np.allclose(np64(c), c64 * np64(keep[2]), rtol=4 * O.U, atol=0)
+    now = a.clone()
+    norm.compute(float("inf"))         # nothing to clip
+    norm.clip_into()
+    assert torch.equal(a, now) and float(norm.record[1]) == 1.0
+
+
+def test_norm_edges():
+    norm = A.GradNorm([(4, "f32"), (0, "bf16")])
+    out = torch.full((4,), 5.0, device="cuda")
+    g = torch.zeros(4, device="cuda")
+    norm.bind([g, None], [out, None])
+    def go(values, max_norm=1.0):
+        g.copy_(torch.tensor(values))
+        norm.compute(max_norm)
+        norm.clip_into()
+        torch.cuda.synchronize()
+        return float(norm.record[0]), float(norm.record[1]), int(norm.nonfinite)
+    assert go([0.0] * 4) == (0.0, 1.0, 0) and not bool(out.any())
+    n, c, bad = go([3e38, 3e38, 0.0, 0.0])       # squares past fp32, the norm past it too
+    # the coefficient 2.4e-39 is a denormal: it is rounded by up to 2^-150
+    true = 1 / np.hypot(np.float64(np.float32(3e38)), np.float64(np.float32(3e38)))
+    assert n == float("inf") and bad == 0 and abs(c - true) <= O.TINY / 2
+    n, c, bad = go([1e-30, 0, 0, 0])             # a square below fp32
+    assert abs(n / 1e-30 - 1) < 4 * O.U and (c, bad) == (1.0, 0)
+    for x in (float("inf"), float("-inf"), float("nan")):
+        n, c, bad = go([1.0, x, 2.0, 3.0])
+        assert (c, bad) == (0.0, 1) and not bool(out.any())
+    assert go([1.0, 0.0, 0.0, 0.0])[1:] == (1.0, 0) and float(out[0]) == 1.0
+    empty = A.GradNorm([(0, "f32")])
+    empty.bind([torch.empty(0, device="cuda")])
+    empty.compute(1.0)
+    assert empty.record.tolist() == [0.0, 1.0]
+
+
+def test_refusals():
+    opt = A.AdamW([A.tensor(8), A.tensor(4, param="bf16")])
+    p = [torch.zeros(8, device="cuda"), torch.zeros(4, device="cuda", dtype=torch.bfloat16)]
+    with pytest.raises(S.ShampooError):
+        opt.step(1e-3)                                    # nothing bound
+    opt.bind(p, p)
+    for bad in ([p[0]], [p[0], None], [p[0], p[0][:4]], [p[0][::2], p[1]], [p[0].cpu(), p[1]],
+                [torch.zeros(16, device="cuda")[::2], p[1]]):
+        with pytest.raises(ValueError):
+            opt.bind(bad)
+    with pytest.raises(S.ShampooError):
+        opt.bind()
+    with pytest.raises(ValueError):
+        opt.step(torch.tensor([1e-3]))
+    with pytest.raises(ValueError):
+        opt.step(torch.tensor([1e-3], device="cuda", dtype=torch.float64))
+    with pytest.raises(S.ShampooError):
+        opt.step(float("nan"))
+    with pytest.raises(S.ShampooError):
+        opt.set_step(-1)
+    norm = A.GradNorm([(4, "bf16")])
+    with pytest.raises(S.ShampooError):
+        norm.compute(1.0)
+    with pytest.raises(ValueError):
+        norm.bind([p[0][:4]])
+    with pytest.raises(ValueError):
+        norm.bind([p[1]], [p[1]])                         # outputs are fp32
+    norm.bind([p[1]])
+    with pytest.raises(S.ShampooError):
+        norm.compute(0.0)
+
+
+# ------------------------------------------------------------ as they are used
+def test_shampoo_and_adamw_under_one_norm():
+    """A model's end of step: bf16 gradients under one norm, matrices on Shampoo
+    with the clipped fp32 gradients, the vectors on AdamW with the coefficient."""
+    rng = np.random.default_rng(17)
+    mats = [(256, 384), (128, 512)]
+    vecs = [384, 512, 1000]
+    mk = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to("cuda", torch.bfloat16)
+    cfg = S.make_config(128, root_mode="auto")
+    shapes = [(r, c, S.DENSE) for r, c in mats]
+    ours, ref = S.Shampoo(shapes, cfg), S.Shampoo(shapes, cfg)
+    W = [torch.zeros(r, c, device="cuda") for r, c in mats]
+    W2 = [w.clone() for w in W]
+    run = Run([A.tensor(n, param="bf16", state_bits=8 if n == 1000 else 32) for n in vecs], 3, warm=False)
+    clipped = [torch.empty(r, c, device="cuda") for r, c in mats]
+    norm = A.GradNorm([(r * c, "bf16") for r, c in mats] + [(n, "bf16") for n in vecs])
+    for t in range(4):
+        G = [mk(r, c) for r, c in mats]
+        for i, n in enumerate(vecs):
+            run.grads[i].copy_(mk(n))
+        before = run.read()
+        norm.bind(G + run.grads, clipped + [None] * len(vecs))
+        norm.compute(1.0)
+        norm.clip_into()
+        ours.step(W, clipped, t, 2)
+        run.opt.step(1e-3, clip=norm)
+        coef = norm.record[1]
+        n64, c64 = O.norm([np64(g).ravel() for g in G + run.grads], 1.0)
+        assert abs(float(coef) - c64) <= 2 * O.U * c64
+        ref.step(W2, [g.float() * coef for g in G], t, 2)
+        for a, b in zip(W, W2):
+            assert torch.equal(a, b)
+        run.check(before, 1e-3, float(coef))
