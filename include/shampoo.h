@@ -495,7 +495,7 @@ typedef struct shampoo_adamw_s shampoo_adamw_t; /* opaque; host memory only */
 
 typedef struct {
     double beta1, beta2;  /* in [0, 1)                                                   */
-    double eps;           /* > 0                                                         */
+    double eps;           /* 2^-100 (8e-31) to 1e30                                      */
     uint32_t seed;        /* of the rounding of 8-bit moments                            */
     int32_t reserved;     /* must be 0                                                   */
 } shampoo_adamw_config;
@@ -525,8 +525,7 @@ typedef struct {
 } shampoo_adamw_layout;
 
 /* Plan for n_tensors tensors.  Host only.  Errors: SHAMPOO_E_ARG (null,
- * n_tensors < 1, numel < 0, a beta outside [0, 1), eps not > 0 in fp32 or not
- * finite, weight_decay or lr_scale negative or not finite, unknown types,
+ * n_tensors < 1, numel < 0, a beta outside [0, 1), eps out of range, weight_decay or lr_scale negative or not finite, unknown types,
  * state_bits not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16
  * weights, numel above 2^38), SHAMPOO_E_NOMEM. */
 int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,

@@ -152,3 +152,37 @@ def norm(grads, max_norm, grad_scale=1.0):
     if not math.isfinite(n):
         return n, 0.0
     return n, grad_scale * min(1.0, max_norm / n if n > 0 else 1.0)
+
+
+# ---------------------------------------------------------------- in fp32
+def step32(p, g, m, v, t, h: Hyper, coef=1.0):
+    """The step in fp32 (NumPy's operations round to nearest): every operation
+    rounded on its own in the order of the formula, scalars formed in fp64 and
+    rounded once.  Returns p, m, root, v."""
+    f = np.float32
+    with np.errstate(all="ignore"):
+        x = g * f(coef)
+        m = m * f(h.beta1) + x * f(1 - h.beta1)
+        v = v * f(h.beta2) + (x * x) * f(1 - h.beta2)
+        root = np.sqrt(v)
+        a = f(h.lr * h.lr_scale * h.weight_decay)
+        b = f(h.lr * h.lr_scale * (1.0 / (1.0 - h.beta1 ** t)))
+        d = root * f(1.0 / np.sqrt(1.0 - h.beta2 ** t)) + f(h.eps)
+        p = p - (p * a + (m / d) * b)
+    return p, m, root, v
+
+
+def codes32(x, r, positive):
+    """Codes and scales of fp32 values (whole runs, finite) in fp32 steps."""
+    f = np.float32
+    y = np.abs(x).reshape(-1, RUN)
+    scale = np.maximum(y.max(1), f(2.0 ** -110)) * f(1 / 448)
+    y = y * (f(1) / scale)[:, None]
+    small = y < f(2.0 ** -6)
+    bits = np.where(small, y + f(2.0 ** -6), y).astype(f).view(np.int32)
+    code = ((bits + (r.reshape(-1, RUN).astype(np.int32) << 4)) >> 20) - np.where(small, 968, 960)
+    if positive:
+        code = np.maximum(code, x.reshape(-1, RUN) > 0)
+    else:
+        code = code + 128 * np.signbit(x).reshape(-1, RUN)
+    return code.astype(np.uint8).reshape(-1), scale

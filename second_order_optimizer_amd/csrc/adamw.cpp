@@ -24,6 +24,7 @@ using namespace shampoo;
 namespace {
 
 constexpr int64_t kMaxNumel = (int64_t)1 << 38;    // runs of a tensor stay below 2^31
+constexpr double kMinEps = 0x1p-100;               // sqrt(v) c + eps is a normal number
 constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -170,7 +171,7 @@ int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,
     if (!cfg || !tensors || !out || n_tensors < 1) return SHAMPOO_E_ARG;
     *out = nullptr;
     if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) ||
-        !(cfg->eps > 0.0 && std::isfinite(cfg->eps)) || (float)cfg->eps == 0.f || cfg->reserved != 0)
+        !(cfg->eps >= kMinEps && cfg->eps <= 1e30) || cfg->reserved != 0)
         return SHAMPOO_E_ARG;
     int64_t tiles = 0;
     for (int i = 0; i < n_tensors; ++i) {

@@ -25,10 +25,11 @@ namespace {
 // anywhere (gfx950 loads and stores 16 bytes at any address).
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned short u16x4u __attribute__((ext_vector_type(4), aligned(2)));
-typedef unsigned short u16x8u __attribute__((ext_vector_type(8), aligned(2)));
-typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // A caller's pointer through the global address space (global, not flat,
 // memory instructions).
@@ -38,92 +39,162 @@ __device__ __forceinline__ T* gptr(uint64_t addr) {
     return (T*)reinterpret_cast<gT*>(addr);
 }
 
-template <int DT> struct Store { typedef unsigned short type; typedef u16x4u vec; };
-template <> struct Store<DT_F32> { typedef float type; typedef f32x4u vec; };
+template <int DT> struct Elem { typedef unsigned short type; };
+template <> struct Elem<DT_F32> { typedef float type; };
 
-__device__ __forceinline__ float widen(unsigned short u, int dt) {
-    if (dt == DT_BF16) return __uint_as_float((uint32_t)u << 16);
-    _Float16 h;
-    __builtin_memcpy(&h, &u, 2);
-    return (float)h;
+template <int DT>
+__device__ __forceinline__ float widen(typename Elem<DT>::type u) {
+    if constexpr (DT == DT_F32) return u;
+    else if constexpr (DT == DT_BF16) return __uint_as_float((uint32_t)u << 16);
+    else {
+        _Float16 h;
+        __builtin_memcpy(&h, &u, 2);
+        return (float)h;
+    }
 }
 
-// Four consecutive elements from `first` of a tensor of `numel`, as fp32;
-// past the end 0.
+// Four elements as they lie in memory: 16 or 8 bytes.
+template <int DT> struct Raw { u32x2 w; };
+template <> struct Raw<DT_F32> { f32x4 w; };
+
 template <int DT>
-__device__ __forceinline__ f32x4 load4(uint64_t base, int64_t first, int64_t numel) {
-    typedef typename Store<DT>::type T;
-    typedef typename Store<DT>::vec V;
-    const T* q = gptr<const T>(base) + first;
-    f32x4 r = {0.f, 0.f, 0.f, 0.f};
-    if (first + 4 <= numel) {
-        const V u = *gptr<const V>((uint64_t)q);
-        for (int k = 0; k < 4; ++k) {
-            if constexpr (DT == DT_F32) r[k] = u[k];
-            else r[k] = widen(u[k], DT);
+__device__ __forceinline__ f32x4 widen4(const Raw<DT>& r) {
+    if constexpr (DT == DT_F32) return r.w;
+    else if constexpr (DT == DT_BF16)
+        return f32x4{__uint_as_float(r.w.x << 16), __uint_as_float(r.w.x & 0xFFFF0000u),
+                     __uint_as_float(r.w.y << 16), __uint_as_float(r.w.y & 0xFFFF0000u)};
+    else {
+        f32x4 x;
+        for (int k = 0; k < 4; ++k) x[k] = widen<DT>((unsigned short)(r.w[k >> 1] >> (16 * (k & 1))));
+        return x;
+    }
+}
+
+// Four consecutive elements from `first` of a tensor; FULL: all four exist,
+// else those past `numel` read as 0.
+template <int DT, bool FULL>
+__device__ __forceinline__ Raw<DT> load4(uint64_t base, int64_t first, int64_t numel) {
+    typedef typename Elem<DT>::type T;
+    const uint64_t at = base + (uint64_t)first * sizeof(T);
+    Raw<DT> r;
+    if constexpr (DT == DT_F32) {
+        if (FULL || first + 4 <= numel) {
+            r.w = *gptr<const f32x4u>(at);
+        } else {
+            for (int k = 0; k < 4; ++k) r.w[k] = first + k < numel ? gptr<const T>(at)[k] : 0.f;
         }
     } else {
-        for (int k = 0; k < 4; ++k)
-            if (first + k < numel) {
-                if constexpr (DT == DT_F32) r[k] = q[k];
-                else r[k] = widen(q[k], DT);
-            }
+        if (FULL || first + 4 <= numel) {
+            r.w = *gptr<const u32x2h>(at);
+        } else {
+            uint32_t u[4];
+            for (int k = 0; k < 4; ++k) u[k] = first + k < numel ? gptr<const T>(at)[k] : 0u;
+            r.w = u32x2{u[0] | u[1] << 16, u[2] | u[3] << 16};
+        }
     }
     return r;
 }
 
-template <typename T, typename V, typename W>
-__device__ __forceinline__ void store4(uint64_t base, int64_t first, int64_t numel, const W& w) {
-    T* q = gptr<T>(base) + first;
-    if (first + 4 <= numel) {
-        V u;
-        for (int k = 0; k < 4; ++k) u[k] = (T)w[k];
-        *gptr<V>((uint64_t)q) = u;
+template <int DT, bool FULL>
+__device__ __forceinline__ void store4(uint64_t base, int64_t first, int64_t numel, const Raw<DT>& r) {
+    typedef typename Elem<DT>::type T;
+    const uint64_t at = base + (uint64_t)first * sizeof(T);
+    if constexpr (DT == DT_F32) {
+        if (FULL || first + 4 <= numel) {
+            *gptr<f32x4u>(at) = r.w;
+        } else {
+            for (int k = 0; k < 4; ++k)
+                if (first + k < numel) gptr<T>(at)[k] = r.w[k];
+        }
     } else {
-        for (int k = 0; k < 4; ++k)
-            if (first + k < numel) q[k] = (T)w[k];
+        if (FULL || first + 4 <= numel) {
+            *gptr<u32x2h>(at) = r.w;
+        } else {
+            for (int k = 0; k < 4; ++k)
+                if (first + k < numel) gptr<T>(at)[k] = (T)(r.w[k >> 1] >> (16 * (k & 1)));
+        }
     }
 }
 
-// The largest of the 32 lanes of a half wave, in each of them.
+// The largest of the 32 lanes of a half wave, in each of them: pairs, quads,
+// eights and rows of 16 by lane permutations inside the ALU, then the two
+// rows of a half exchanged.  All 64 lanes active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
 __device__ __forceinline__ uint32_t half_max(uint32_t v) {
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint32_t w = (uint32_t)__shfl_xor((int)v, o, 64);
-        v = v > w ? v : w;
-    }
-    return v;
+    v = umax(v, moved<0xB1>(v));    // quad_perm [1,0,3,2]
+    v = umax(v, moved<0x4E>(v));    // quad_perm [2,3,0,1]
+    v = umax(v, moved<0x141>(v));   // the other quad of eight
+    v = umax(v, moved<0x140>(v));   // the other eight of a row
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return umax(r[0], r[1]);
+}
+
+// 1/d rounded to nearest, for normal d and 1/d: one Newton step on the
+// hardware's reciprocal (equal to 1/d for every significand and every
+// exponent from -125 to 125, counted on the card).
+__device__ __forceinline__ float reciprocal(float d) {
+    const float y = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, y, 1.f), y, y);
+}
+// m/d rounded to nearest: the quotient by the rounded reciprocal is within
+// one unit, and its remainder, exact in one fma, decides (Markstein 1990).
+// d: positive and normal, or infinite, which stands for 2^126 here: the
+// quotient is then not 0 but at most 2^-127 of m.
+__device__ __forceinline__ float quotient(float m, float d) {
+    d = fminf(d, 0x1p126f);
+    const float y = reciprocal(d);
+    const float q = m * y;
+    return __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
+}
+// sqrt(v) rounded to nearest for v = 0 and 2^-96 <= v < infinity: one
+// correction of v / sqrt(v) (equal to the rounded root for every significand
+// and every exponent of that range, counted on the card).
+constexpr uint32_t kRootLow = 0x0F800000u;   // 2^-96
+__device__ __forceinline__ float near_root(float v) {
+    const float y = __builtin_amdgcn_rsqf(__uint_as_float(umax(__float_as_uint(v), kRootLow)));
+    const float r = v * y;
+    return __builtin_fmaf(__builtin_fmaf(-r, r, v), 0.5f * y, r);
 }
 
 // Scale of a run from the largest magnitude among its finite values, and the
-// factor that takes values to e4m3's range (up to 448).  The floor keeps the
-// factor finite; values below it are kept as they fall under that scale.
+// factor that takes values to e4m3's range (up to 448, and up to 3 units in
+// the last place past it).  The floor keeps the factor finite; values below
+// it are kept as they fall under that scale.
 __device__ __forceinline__ void run_scale(uint32_t amax_bits, float& scale, float& inv) {
     scale = fmaxf(__uint_as_float(amax_bits), 0x1p-110f) * (1.0f / 448);
-    inv = 1.0f / scale;
+    inv = reciprocal(scale);
 }
 
 constexpr uint32_t kFinite = 0x7F7FFFFFu;
 
-// One value as an e4m3 code (without sign): y = |x| inv in [0, 448].  Rounded
-// up with the probability of the fraction that e4m3 drops (r: 16 random bits
-// shifted to the top of the 20 mantissa bits that it drops), so that moving
-// averages whose change in one step is less than half a code still move.
-// Below 2^-6 e4m3 steps evenly, as it does in [2^-6, 2^-5): adding 2^-6 puts
-// those values there.  A value that is not finite becomes NaN.
-template <bool POSITIVE>
+// The magnitude of one finite value as an e4m3 code in the top byte (bit 31
+// clear).  y = |x| inv in [0, 448].  Rounded up with the probability of the
+// fraction that e4m3 drops, so that moving averages whose change in one step
+// is less than half a code still move: `r` holds 16 random bits in bits 8 to
+// 23, at the top of the 20 mantissa bits that e4m3 drops (4 places up), and
+// 0x40, which is -960 = -(120 << 3) mod 256, the exponents' difference in
+// bias, in the top byte.  Below 2^-6 e4m3 steps evenly, as fp32 rounded to
+// three bits does in [2^-6, 2^-5): (y + 2^-6) / 2 has the code 8 less that
+// belongs there, is larger than y below 2^-6 and smaller above.  The sum does
+// not carry past code 126: its random part is at most 2^20 - 16 of 2^20.
 __device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t r) {
     const float y = fabsf(x) * inv;
-    const bool small = y < 0x1p-6f;
-    const uint32_t b = __float_as_uint(small ? y + 0x1p-6f : y);
-    uint32_t c = ((b + r) >> 20) - (small ? 968u : 960u);
-    c = c < 126u ? c : 126u;
-    // a positive root never becomes 0, whose division would be by eps alone
-    if (POSITIVE) {
-        if (x > 0.f && c == 0u) c = 1u;
-    }
-    if ((__float_as_uint(x) & 0x7FFFFFFFu) > kFinite) c = 127u;
-    if (!POSITIVE) c |= (__float_as_uint(x) >> 24) & 128u;
-    return c;
+    const float z = fmaxf(y, __builtin_fmaf(y, 0.5f, 0x1p-7f));
+    return (__float_as_uint(z) << 4) + r;
+}
+// Where a run holds values that are not finite: those become NaN, code 127.
+__device__ __forceinline__ uint32_t encode_any(float x, float inv, uint32_t r) {
+    const bool finite = (__float_as_uint(x) & 0x7FFFFFFFu) <= kFinite;
+    const uint32_t c = encode(finite ? x : 0.f, inv, r);
+    return finite ? c : 0x7F000000u;
+}
+// The top bytes of four words, as one word.
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t* w) {
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w[3], w[2], 0x07030c0cu),
+                                 __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0703u), 0x07060100u);
 }
 
 __device__ __forceinline__ f32x4 decode4(uint32_t w) {
@@ -133,9 +204,180 @@ __device__ __forceinline__ f32x4 decode4(uint32_t w) {
     return f32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// One step of the elements of this wave's tiles.  Half a wave takes a run of
-// 256 elements: lane l the elements 4l.. and 128 + 4l.., so that every load
-// and store of the half covers whole 128-byte lines.
+// The codes of this lane's eight elements.  ANY: some value of the half's run
+// is not finite.
+template <bool ANY>
+__device__ __forceinline__ void encode_run(const AdamwArgs& a, const f32x4* m, const f32x4* root, float mi,
+                                           float si, uint32_t key, uint32_t e0, int64_t st) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t mc[4], sc[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t h = mix32(key ^ (e0 + 128 * j + q));
+            // from the top byte down: 0x40, half of the hash, 0
+            const uint32_t rm = __builtin_amdgcn_perm(0x40000000u, h, 0x0701000cu);
+            const uint32_t rs = __builtin_amdgcn_perm(0x40000000u, h, 0x0703020cu);
+            const float x = m[j][q], y = root[j][q];
+            mc[q] = ANY ? encode_any(x, mi, rm) : encode(x, mi, rm);
+            sc[q] = ANY ? encode_any(y, si, rs) : encode(y, si, rs);
+            mc[q] = (mc[q] & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
+            // a positive root never becomes 0, whose division would be by eps
+            // alone: code 1 at least, unless the root is 0
+            const uint32_t yb = __float_as_uint(y);
+            sc[q] = umax(sc[q], yb < 0x01000000u ? yb : 0x01000000u);
+        }
+        *reinterpret_cast<uint32_t*>(a.m8 + st + 128 * j) = top_bytes(mc);
+        *reinterpret_cast<uint32_t*>(a.s8 + st + 128 * j) = top_bytes(sc);
+    }
+}
+
+// One run of 256 elements by half a wave: lane l (of 32) takes the elements
+// 4l.. and 128 + 4l.., so that every load and store of the half covers whole
+// 128-byte lines.
+template <int P, int G, bool S8, bool FULL>
+__device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& ts, int64_t run, int l,
+                                         float coef, float fa, float fb, float root_c, uint32_t key) {
+    const int64_t sr = ts.state_run + run;
+    const int64_t st = sr * kRun + 4 * l;
+    const int64_t e0 = run * kRun + 4 * l;
+    const int64_t rm = (ts.rem_run + run) * kRun + 4 * l;
+    Raw<G> graw[2];
+    Raw<P> praw[2];
+    u32x2 rem[2];
+    uint32_t mw[2], sw[2];
+    f32x4 m[2], v[2];
+    float ms = 0.f, ss = 0.f;
+    if constexpr (S8) {
+        ms = a.m_scale[sr];
+        ss = a.s_scale[sr];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        graw[j] = load4<G, FULL>(ts.g_ptr, e0 + 128 * j, ts.numel);
+        praw[j] = load4<P, FULL>(ts.p_ptr, e0 + 128 * j, ts.numel);
+        if constexpr (P == DT_BF16) rem[j] = *reinterpret_cast<const u32x2*>(a.rem + rm + 128 * j);
+        if constexpr (S8) {
+            mw[j] = *reinterpret_cast<const uint32_t*>(a.m8 + st + 128 * j);
+            sw[j] = *reinterpret_cast<const uint32_t*>(a.s8 + st + 128 * j);
+        } else {
+            m[j] = *reinterpret_cast<const f32x4*>(a.m + st + 128 * j);
+            v[j] = *reinterpret_cast<const f32x4*>(a.v + st + 128 * j);
+        }
+    }
+    uint32_t tmin = 0xFFFFFFFFu, tmax = 0u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const f32x4 g = widen4<G>(graw[j]);
+        if constexpr (S8) {
+            m[j] = decode4(mw[j]);
+            v[j] = decode4(sw[j]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float x = g[q] * coef;
+            if constexpr (S8) {
+                m[j][q] = m[j][q] * ms;
+                v[j][q] = v[j][q] * ss;
+                v[j][q] = v[j][q] * v[j][q];
+            }
+            m[j][q] = m[j][q] * a.b1 + x * a.c1;
+            v[j][q] = v[j][q] * a.b2 + (x * x) * a.c2;
+            const uint32_t b = __float_as_uint(v[j][q]);
+            tmin = tmin < b - 1 ? tmin : b - 1;   // 0 counts as the largest
+            tmax = umax(tmax, b);
+        }
+    }
+    f32x4 root[2];
+    if (__any(tmin < kRootLow - 1 || tmax > kFinite)) {
+        for (int j = 0; j < 2; ++j)
+            for (int q = 0; q < 4; ++q) root[j][q] = sqrtf(v[j][q]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) root[j][q] = near_root(v[j][q]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        Raw<P> out;
+        u32x2 left;
+        f32x4 w;
+        if constexpr (P == DT_BF16) {
+            // bits = (hi << 16) + the signed remainder
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t hi = q & 1 ? praw[j].w[q >> 1] & 0xFFFF0000u : praw[j].w[q >> 1] << 16;
+                const uint32_t r = q & 1 ? (uint32_t)((int)rem[j][q >> 1] >> 16)
+                                         : (uint32_t)(int)(short)rem[j][q >> 1];
+                w[q] = __uint_as_float(hi + r);
+            }
+        } else {
+            w = praw[j].w;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float d = root[j][q] * root_c + a.eps;
+            w[q] = w[q] - (w[q] * fa + quotient(m[j][q], d) * fb);
+        }
+        if constexpr (P == DT_BF16) {
+            // the nearest bf16 (ties away from zero) is the upper half of bits +
+            // 2^15, and what is left, as a signed number, is the lower half of
+            // bits; a NaN becomes the quiet NaN without remainder
+            uint32_t b[4];
+            for (int q = 0; q < 4; ++q)
+                b[q] = w[q] != w[q] ? 0x7FC00000u : __float_as_uint(w[q]);
+            for (int k = 0; k < 2; ++k) {
+                out.w[k] = __builtin_amdgcn_perm(b[2 * k + 1] + 0x8000u, b[2 * k] + 0x8000u, 0x07060302u);
+                left[k] = __builtin_amdgcn_perm(b[2 * k + 1], b[2 * k], 0x05040100u);
+            }
+            *reinterpret_cast<u32x2*>(a.rem + rm + 128 * j) = left;
+        } else {
+            out.w = w;
+        }
+        store4<P, FULL>(ts.p_ptr, e0 + 128 * j, ts.numel, out);
+        if constexpr (!S8) {
+            *reinterpret_cast<f32x4*>(a.m + st + 128 * j) = m[j];
+            *reinterpret_cast<f32x4*>(a.v + st + 128 * j) = v[j];
+        }
+    }
+    if constexpr (S8) {
+        uint32_t mmax = 0, smax = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                mmax = umax(mmax, __float_as_uint(m[j][q]) & 0x7FFFFFFFu);
+                smax = umax(smax, __float_as_uint(root[j][q]) & 0x7FFFFFFFu);
+            }
+        mmax = half_max(mmax);
+        smax = half_max(smax);
+        const bool any = __any(umax(mmax, smax) > kFinite);
+        if (any) {   // the scales are those of the finite values
+            mmax = smax = 0;
+            for (int j = 0; j < 2; ++j)
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t mb = __float_as_uint(m[j][q]) & 0x7FFFFFFFu;
+                    const uint32_t sb = __float_as_uint(root[j][q]) & 0x7FFFFFFFu;
+                    mmax = umax(mmax, mb <= kFinite ? mb : 0u);
+                    smax = umax(smax, sb <= kFinite ? sb : 0u);
+                }
+            mmax = half_max(mmax);
+            smax = half_max(smax);
+        }
+        float mi, si;
+        run_scale(mmax, ms, mi);
+        run_scale(smax, ss, si);
+        if (l == 0) {
+            a.m_scale[sr] = ms;
+            a.s_scale[sr] = ss;
+        }
+        key += (uint32_t)((uint64_t)e0 >> 32) * 0x85157AF5u;
+        if (any) encode_run<true>(a, m, root, mi, si, key, (uint32_t)e0, st);
+        else encode_run<false>(a, m, root, mi, si, key, (uint32_t)e0, st);
+    }
+}
+
+// One step of the elements of this wave's tiles.
 template <int P, int G, bool S8>
 __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
     const AdamwClock clk = a.clocks[blockIdx.x];
@@ -144,7 +386,6 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         if (a.clip->nonfinite) return;   // the same for every workgroup: nothing changes
         coef = a.clip->coef;
     }
-    __syncthreads();   // every wave has read the clock
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
     const int lane = threadIdx.x & 63, l = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -155,104 +396,18 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         if (!ts.g_ptr) continue;
         const float fa = (float)(lr * ts.lr_scale * ts.weight_decay);
         const float fb = (float)(lr * ts.lr_scale * clk.inv1);
-        const uint32_t key1 = mix32(key0 + (uint32_t)ts.id);
-        for (int k = lane >> 5; k < tl.nruns; k += 2) {
-            const int64_t run = tl.run0 + k;
-            const int64_t st = (ts.state_run + run) * kRun;
-            f32x4 p[2], m[2], v[2], g[2];
-            i16x4 rem[2];
-            float ms = 0.f, ss = 0.f;
-            if constexpr (S8) {
-                ms = a.m_scale[ts.state_run + run];
-                ss = a.s_scale[ts.state_run + run];
-            }
-            for (int j = 0; j < 2; ++j) {
-                const int o = 128 * j + 4 * l;
-                const int64_t e = run * kRun + o;
-                g[j] = load4<G>(ts.g_ptr, e, ts.numel);
-                p[j] = load4<P>(ts.p_ptr, e, ts.numel);
-                if constexpr (P == DT_BF16)
-                    rem[j] = *reinterpret_cast<const i16x4*>(a.rem + (ts.rem_run + run) * kRun + o);
-                if constexpr (S8) {
-                    m[j] = decode4(*reinterpret_cast<const uint32_t*>(a.m8 + st + o));
-                    v[j] = decode4(*reinterpret_cast<const uint32_t*>(a.s8 + st + o));
-                } else {
-                    m[j] = *reinterpret_cast<const f32x4*>(a.m + st + o);
-                    v[j] = *reinterpret_cast<const f32x4*>(a.v + st + o);
-                }
-            }
-            uint32_t mmax = 0, smax = 0;
-            for (int j = 0; j < 2; ++j)
-                for (int q = 0; q < 4; ++q) {
-                    const float x = g[j][q] * coef;
-                    float m0 = m[j][q], v0 = v[j][q];
-                    if constexpr (S8) {
-                        m0 = m0 * ms;
-                        v0 = v0 * ss;
-                        v0 = v0 * v0;
-                    }
-                    const float m1 = m0 * a.b1 + x * a.c1;
-                    const float v1 = v0 * a.b2 + (x * x) * a.c2;
-                    const float root = sqrtf(v1);
-                    const float d = root * clk.inv_root2 + a.eps;
-                    float w = p[j][q];
-                    if constexpr (P == DT_BF16)
-                        w = __uint_as_float(__float_as_uint(w) + (uint32_t)(int)rem[j][q]);
-                    w = w - (w * fa + (m1 / d) * fb);
-                    p[j][q] = w;
-                    m[j][q] = m1;
-                    v[j][q] = S8 ? root : v1;
-                    if constexpr (S8) {
-                        const uint32_t mb = __float_as_uint(m1) & 0x7FFFFFFFu;
-                        const uint32_t sb = __float_as_uint(root) & 0x7FFFFFFFu;
-                        if (mb <= kFinite) mmax = mmax > mb ? mmax : mb;
-                        if (sb <= kFinite) smax = smax > sb ? smax : sb;
-                    }
-                }
-            float mi = 0.f, si = 0.f;
-            if constexpr (S8) {
-                run_scale(half_max(mmax), ms, mi);
-                run_scale(half_max(smax), ss, si);
-                if (l == 0) {
-                    a.m_scale[ts.state_run + run] = ms;
-                    a.s_scale[ts.state_run + run] = ss;
-                }
-            }
-            for (int j = 0; j < 2; ++j) {
-                const int o = 128 * j + 4 * l;
-                const int64_t e = run * kRun + o;
-                if constexpr (P == DT_BF16) {
-                    u16x4 hi;
-                    for (int q = 0; q < 4; ++q) {
-                        // nearest bf16 (ties away from zero); what is left fits 16 bits
-                        const uint32_t b = __float_as_uint(p[j][q]);
-                        const uint32_t h = (b + 0x8000u) >> 16;
-                        const bool nan = (b & 0x7FFFFFFFu) > 0x7F800000u;
-                        hi[q] = nan ? (unsigned short)0x7FC0 : (unsigned short)h;
-                        rem[j][q] = nan ? (short)0 : (short)(b - (h << 16));
-                    }
-                    store4<unsigned short, u16x4u>(ts.p_ptr, e, ts.numel, hi);
-                    *reinterpret_cast<i16x4*>(a.rem + (ts.rem_run + run) * kRun + o) = rem[j];
-                } else {
-                    store4<float, f32x4u>(ts.p_ptr, e, ts.numel, p[j]);
-                }
-                if constexpr (S8) {
-                    uint32_t mw = 0, sw = 0;
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t key = key1 + (uint32_t)((uint64_t)e >> 32) * 0x85157AF5u;
-                        const uint32_t h = mix32(key ^ ((uint32_t)e + q));
-                        mw |= encode<false>(m[j][q], mi, (h & 0xFFFFu) << 4) << (8 * q);
-                        sw |= encode<true>(v[j][q], si, (h >> 16) << 4) << (8 * q);
-                    }
-                    *reinterpret_cast<uint32_t*>(a.m8 + st + o) = mw;
-                    *reinterpret_cast<uint32_t*>(a.s8 + st + o) = sw;
-                } else {
-                    *reinterpret_cast<f32x4*>(a.m + st + o) = m[j];
-                    *reinterpret_cast<f32x4*>(a.v + st + o) = v[j];
-                }
-            }
+        const uint32_t key = mix32(key0 + (uint32_t)ts.id);
+        // two runs at a time, one to each half; an odd last run is taken by
+        // both halves' lanes together with a run that has no elements
+        for (int k = 0; k < tl.nruns; k += 2) {
+            const int64_t run = tl.run0 + k + (lane >> 5);
+            if ((tl.run0 + k + 2) * kRun <= ts.numel)
+                step_run<P, G, S8, true>(a, ts, run, l, coef, fa, fb, clk.inv_root2, key);
+            else if (run * kRun < ts.numel)
+                step_run<P, G, S8, false>(a, ts, run, l, coef, fa, fb, clk.inv_root2, key);
         }
     }
+    __syncthreads();   // every wave has read the clock
     if (threadIdx.x == 0) {
         AdamwClock n = clk;
         n.t += 1;
@@ -304,7 +459,7 @@ __device__ __forceinline__ double tile_squares(uint64_t g, int64_t first, int64_
     double s[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kNormTile / 256; ++k) {
-        const f32x4 x = load4<DT>(g, first + k * 256 + lane * 4, numel);
+        const f32x4 x = widen4<DT>(load4<DT, false>(g, first + k * 256 + lane * 4, numel));
         for (int q = 0; q < 4; ++q) s[q] += (double)x[q] * (double)x[q];
     }
     return (s[0] + s[1]) + (s[2] + s[3]);
@@ -360,9 +515,10 @@ __device__ __forceinline__ void tile_clip(const NormTensor& ts, int64_t first, i
 #pragma unroll
     for (int k = 0; k < kNormTile / 256; ++k) {
         const int64_t e = first + k * 256 + lane * 4;
-        f32x4 x = load4<DT>(ts.g_ptr, e, ts.numel);
-        for (int q = 0; q < 4; ++q) x[q] = zero ? 0.f : x[q] * coef;
-        store4<float, f32x4u>(ts.out_ptr, e, ts.numel, x);
+        const f32x4 x = widen4<DT>(load4<DT, false>(ts.g_ptr, e, ts.numel));
+        Raw<DT_F32> y;
+        for (int q = 0; q < 4; ++q) y.w[q] = zero ? 0.f : x[q] * coef;
+        store4<DT_F32, false>(ts.out_ptr, e, ts.numel, y);
     }
 }
 

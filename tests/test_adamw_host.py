@@ -47,7 +47,7 @@ def test_adamw_create_refuses_tensor(field, value, rc):
 
 @pytest.mark.parametrize("field,value", [
     ("beta1", 1.0), ("beta1", -0.1), ("beta2", 1.0), ("beta2", float("nan")), ("eps", 0.0),
-    ("eps", -1e-8), ("eps", float("inf")), ("eps", float("nan")), ("eps", 1e-60), ("reserved", 1)])
+    ("eps", -1e-8), ("eps", float("inf")), ("eps", float("nan")), ("eps", 1e-60), ("eps", 7e-31), ("eps", 1e31), ("reserved", 1)])
 def test_adamw_create_refuses_config(field, value):
     c = A.make_config()
     setattr(c, field, value)

@@ -251,6 +251,49 @@ def test_range_of_gradients(exponent):
         run.check(before, 1e-3)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", ["usual", "wide", "low", "zeros"])
+def test_every_rounding(kind, bits):
+    """Bit for bit the fp32 operations of the formula, each rounded to nearest,
+    over the range of fp32: roots of denormal and of huge second moments, small
+    and large quotients."""
+    n = 64 * 256
+    rng = np.random.default_rng(len(kind))
+    lo, hi = {"usual": (-3, 0), "wide": (-21, 18), "low": (-24, -12), "zeros": (-6, 0)}[kind]
+    draw = lambda: (rng.standard_normal(n) * 10.0 ** rng.uniform(lo, hi, n)).astype(np.float32)
+    h = O.Hyper(lr=1e-3, weight_decay=0.1, eps=1e-25 if kind == "low" else 1e-8)
+    opt = A.AdamW([A.tensor(n, state_bits=bits, weight_decay=0.1)], A.make_config(eps=h.eps, seed=9))
+    w = rng.standard_normal(n).astype(np.float32)
+    m, v = np.zeros(n, np.float32), np.zeros(n, np.float32)
+    p, g = torch.from_numpy(w.copy()).cuda(), torch.zeros(n, device="cuda")
+    opt.bind([p], [g])
+    held = opt.state_tensors()
+    same = lambda a, b: np.array_equal(np.asarray(a).view(np.uint32), np.asarray(b).view(np.uint32))
+    for t in (1, 2, 3):
+        x = draw()
+        if kind == "zeros":
+            x[rng.random(n) < 0.5] = 0.0
+        g.copy_(torch.from_numpy(x))
+        opt.step(h.lr)
+        w, m, root, v = O.step32(w, x, m, v, t, h)
+        assert np.isfinite(v).all()
+        assert same(p.cpu().numpy(), w), t
+        if bits == 32:
+            assert same(held["m"].cpu().numpy(), m) and same(held["v"].cpu().numpy(), v)
+            continue
+        rm, rs = O.random_bits(9, t, 0, np.arange(n))
+        for value, r, code, scale, pos in ((m, rm, "m8", "m_scale", False), (root, rs, "s8", "s_scale", True)):
+            c, s = O.codes32(value, r, pos)
+            assert same(held[scale].cpu().numpy(), s), (t, scale)
+            assert np.array_equal(held[code].view(torch.uint8).cpu().numpy(), c), (t, code)
+        spread = lambda k: np.repeat(held[k].cpu().numpy(), 256)
+        dec = lambda k: O.decode(held[k].view(torch.uint8).cpu().numpy()).astype(np.float32)
+        with np.errstate(under="ignore"):
+            m = dec("m8") * spread("m_scale")
+            root = dec("s8") * spread("s_scale")
+            v = root * root
+
+
 def test_many_tensors_of_mixed_kinds():
     """More tensors than one launch of the pointer kernel carries, every kind of
     them in one plan, some without a gradient."""
