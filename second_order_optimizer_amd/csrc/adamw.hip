@@ -30,6 +30,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // A caller's pointer through the global address space (global, not flat,
 // memory instructions).
@@ -37,6 +38,18 @@ template <typename T>
 __device__ __forceinline__ T* gptr(uint64_t addr) {
     typedef __attribute__((address_space(1))) T gT;
     return (T*)reinterpret_cast<gT*>(addr);
+}
+
+// One load or store, past the caches' retention (NT) or not.
+template <bool NT, typename T>
+__device__ __forceinline__ T ld(const T* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void st(T* p, T x) {
+    if constexpr (NT) __builtin_nontemporal_store(x, p);
+    else *p = x;
 }
 
 template <int DT> struct Elem { typedef unsigned short type; };
@@ -72,20 +85,20 @@ __device__ __forceinline__ f32x4 widen4(const Raw<DT>& r) {
 
 // Four consecutive elements from `first` of a tensor; FULL: all four exist,
 // else those past `numel` read as 0.
-template <int DT, bool FULL>
+template <int DT, bool FULL, bool NT = false>
 __device__ __forceinline__ Raw<DT> load4(uint64_t base, int64_t first, int64_t numel) {
     typedef typename Elem<DT>::type T;
     const uint64_t at = base + (uint64_t)first * sizeof(T);
     Raw<DT> r;
     if constexpr (DT == DT_F32) {
         if (FULL || first + 4 <= numel) {
-            r.w = *gptr<const f32x4u>(at);
+            r.w = ld<NT>(gptr<const f32x4u>(at));
         } else {
             for (int k = 0; k < 4; ++k) r.w[k] = first + k < numel ? gptr<const T>(at)[k] : 0.f;
         }
     } else {
         if (FULL || first + 4 <= numel) {
-            r.w = *gptr<const u32x2h>(at);
+            r.w = ld<NT>(gptr<const u32x2h>(at));
         } else {
             uint32_t u[4];
             for (int k = 0; k < 4; ++k) u[k] = first + k < numel ? gptr<const T>(at)[k] : 0u;
@@ -95,20 +108,20 @@ __device__ __forceinline__ Raw<DT> load4(uint64_t base, int64_t first, int64_t n
     return r;
 }
 
-template <int DT, bool FULL>
+template <int DT, bool FULL, bool NT = false>
 __device__ __forceinline__ void store4(uint64_t base, int64_t first, int64_t numel, const Raw<DT>& r) {
     typedef typename Elem<DT>::type T;
     const uint64_t at = base + (uint64_t)first * sizeof(T);
     if constexpr (DT == DT_F32) {
         if (FULL || first + 4 <= numel) {
-            *gptr<f32x4u>(at) = r.w;
+            st<NT>(gptr<f32x4u>(at), (f32x4u)r.w);
         } else {
             for (int k = 0; k < 4; ++k)
                 if (first + k < numel) gptr<T>(at)[k] = r.w[k];
         }
     } else {
         if (FULL || first + 4 <= numel) {
-            *gptr<u32x2h>(at) = r.w;
+            st<NT>(gptr<u32x2h>(at), (u32x2h)r.w);
         } else {
             for (int k = 0; k < 4; ++k)
                 if (first + k < numel) gptr<T>(at)[k] = (T)(r.w[k >> 1] >> (16 * (k & 1)));
@@ -116,20 +129,28 @@ __device__ __forceinline__ void store4(uint64_t base, int64_t first, int64_t num
     }
 }
 
-// The largest of the 32 lanes of a half wave, in each of them: pairs, quads,
-// eights and rows of 16 by lane permutations inside the ALU, then the two
-// rows of a half exchanged.  All 64 lanes active.
+// Lane permutations inside the ALU.  A half wave is two rows of 16 lanes.
 template <int CTRL>
 __device__ __forceinline__ uint32_t moved(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
-__device__ __forceinline__ uint32_t half_max(uint32_t v) {
+// The largest `a` of the half in the lanes of its first row, the largest `b`
+// in those of its second: the rows' halves are exchanged first, so that one
+// reduction does for both.  The lanes of a half are active together.
+__device__ __forceinline__ uint32_t half_max2(uint32_t a, uint32_t b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    uint32_t v = umax(r[0], r[1]);
     v = umax(v, moved<0xB1>(v));    // quad_perm [1,0,3,2]
     v = umax(v, moved<0x4E>(v));    // quad_perm [2,3,0,1]
     v = umax(v, moved<0x141>(v));   // the other quad of eight
-    v = umax(v, moved<0x140>(v));   // the other eight of a row
-    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return umax(r[0], r[1]);
+    return umax(v, moved<0x140>(v));   // the other eight of the row
+}
+// What the first and the second row hold (each the same in its 16 lanes), to
+// all lanes of the half.
+__device__ __forceinline__ void half_both(float v, float& first, float& second) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    first = __uint_as_float(r[0]);
+    second = __uint_as_float(r[1]);
 }
 
 // 1/d rounded to nearest, for normal d and 1/d: one Newton step on the
@@ -141,17 +162,16 @@ __device__ __forceinline__ float reciprocal(float d) {
 }
 // m/d rounded to nearest: the quotient by the rounded reciprocal is within
 // one unit, and its remainder, exact in one fma, decides (Markstein 1990).
-// d: positive and normal, or infinite, which stands for 2^126 here: the
-// quotient is then not 0 but at most 2^-127 of m.
+// d: positive, normal, below 2^126.
 __device__ __forceinline__ float quotient(float m, float d) {
-    d = fminf(d, 0x1p126f);
     const float y = reciprocal(d);
     const float q = m * y;
     return __builtin_fmaf(__builtin_fmaf(-d, q, m), y, q);
 }
 // sqrt(v) rounded to nearest for v = 0 and 2^-96 <= v < infinity: one
 // correction of v / sqrt(v) (equal to the rounded root for every significand
-// and every exponent of that range, counted on the card).
+// and every exponent of that range, counted on the card).  NaN for v that is
+// not finite.
 constexpr uint32_t kRootLow = 0x0F800000u;   // 2^-96
 __device__ __forceinline__ float near_root(float v) {
     const float y = __builtin_amdgcn_rsqf(__uint_as_float(umax(__float_as_uint(v), kRootLow)));
@@ -170,26 +190,24 @@ __device__ __forceinline__ void run_scale(uint32_t amax_bits, float& scale, floa
 
 constexpr uint32_t kFinite = 0x7F7FFFFFu;
 
-// The magnitude of one finite value as an e4m3 code in the top byte (bit 31
-// clear).  y = |x| inv in [0, 448].  Rounded up with the probability of the
-// fraction that e4m3 drops, so that moving averages whose change in one step
-// is less than half a code still move: `r` holds 16 random bits in bits 8 to
-// 23, at the top of the 20 mantissa bits that e4m3 drops (4 places up), and
-// 0x40, which is -960 = -(120 << 3) mod 256, the exponents' difference in
-// bias, in the top byte.  Below 2^-6 e4m3 steps evenly, as fp32 rounded to
-// three bits does in [2^-6, 2^-5): (y + 2^-6) / 2 has the code 8 less that
-// belongs there, is larger than y below 2^-6 and smaller above.  The sum does
-// not carry past code 126: its random part is at most 2^20 - 16 of 2^20.
-__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t r) {
-    const float y = fabsf(x) * inv;
-    const float z = fmaxf(y, __builtin_fmaf(y, 0.5f, 0x1p-7f));
-    return (__float_as_uint(z) << 4) + r;
-}
-// Where a run holds values that are not finite: those become NaN, code 127.
+// A value x becomes an e4m3 code of y = x inv, |y| <= 448, rounded to the code
+// above in magnitude with the probability of the fraction that e4m3 drops, so
+// that moving averages whose change in one step is less than half a code still
+// move: 16 random bits are added at the top of the 20 mantissa bits that are
+// dropped.  Their sum does not carry past code 126: the random part is at most
+// 2^20 - 16 of 2^20.  The hardware's conversion does this for |y| >= 2^-6.
+//
+// Below 2^-6 e4m3 steps evenly, as fp32 rounded to three bits does in [2^-6,
+// 2^-5): there y counts as y + 2^-6 in fp32.  In integers, with the code in
+// the top byte and bit 31 clear: (y + 2^-6) / 2 has the code 8 less that
+// belongs there, is larger than y below 2^-6 and smaller above; r holds the
+// random bits in bits 8 to 23 and 0x40 = -(120 << 3) mod 256, the difference
+// in bias, in the top byte.  A value that is not finite becomes NaN, code 127.
 __device__ __forceinline__ uint32_t encode_any(float x, float inv, uint32_t r) {
     const bool finite = (__float_as_uint(x) & 0x7FFFFFFFu) <= kFinite;
-    const uint32_t c = encode(finite ? x : 0.f, inv, r);
-    return finite ? c : 0x7F000000u;
+    const float y = finite ? fabsf(x) * inv : 0.f;
+    const float z = fmaxf(y, __builtin_fmaf(y, 0.5f, 0x1p-7f));
+    return finite ? (__float_as_uint(z) << 4) + r : 0x7F000000u;
 }
 // The top bytes of four words, as one word.
 __device__ __forceinline__ uint32_t top_bytes(const uint32_t* w) {
@@ -204,42 +222,56 @@ __device__ __forceinline__ f32x4 decode4(uint32_t w) {
     return f32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// The codes of this lane's eight elements.  ANY: some value of the half's run
-// is not finite.
-template <bool ANY>
+// The codes of this lane's eight elements.  `start`: the hash's input of the
+// first one after the first shift-xor; those of the others differ by their
+// offset, in bits that the shift does not reach.  ANY: the run holds values
+// below 2^-6 of e4m3's range or not finite.
+template <bool ANY, bool NT>
 __device__ __forceinline__ void encode_run(const AdamwArgs& a, const f32x4* m, const f32x4* root, float mi,
-                                           float si, uint32_t key, uint32_t e0, int64_t st) {
+                                           float si, uint32_t start, int64_t at) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t mc[4], sc[4];
+        uint32_t h[4], mw = 0, sw = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t h = mix32(key ^ (e0 + 128 * j + q));
-            // from the top byte down: 0x40, half of the hash, 0
-            const uint32_t rm = __builtin_amdgcn_perm(0x40000000u, h, 0x0701000cu);
-            const uint32_t rs = __builtin_amdgcn_perm(0x40000000u, h, 0x0703020cu);
-            const float x = m[j][q], y = root[j][q];
-            mc[q] = ANY ? encode_any(x, mi, rm) : encode(x, mi, rm);
-            sc[q] = ANY ? encode_any(y, si, rs) : encode(y, si, rs);
-            mc[q] = (mc[q] & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
-            // a positive root never becomes 0, whose division would be by eps
-            // alone: code 1 at least, unless the root is 0
-            const uint32_t yb = __float_as_uint(y);
-            sc[q] = umax(sc[q], yb < 0x01000000u ? yb : 0x01000000u);
+        for (int q = 0; q < 4; ++q) h[q] = mix32_rest(start ^ (uint32_t)(128 * j + q));
+        if constexpr (ANY) {
+            uint32_t mc[4], sc[4];
+            for (int q = 0; q < 4; ++q) {
+                const float x = m[j][q], y = root[j][q];
+                // from the top byte down: 0x40, half of the hash, 0
+                mc[q] = encode_any(x, mi, __builtin_amdgcn_perm(0x40000000u, h[q], 0x0701000cu));
+                sc[q] = encode_any(y, si, __builtin_amdgcn_perm(0x40000000u, h[q], 0x0703020cu));
+                mc[q] = (mc[q] & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
+                // a positive root never becomes 0, whose division would be by
+                // eps alone: code 1 at least, unless the root is 0
+                const uint32_t yb = __float_as_uint(y);
+                sc[q] = umax(sc[q], yb < 0x01000000u ? yb : 0x01000000u);
+            }
+            mw = top_bytes(mc);
+            sw = top_bytes(sc);
+        } else {
+            mw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(m[j][0] * mi, h[0] << 16, (int)mw, 0);
+            mw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(m[j][1] * mi, h[1] << 16, (int)mw, 1);
+            mw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(m[j][2] * mi, h[2] << 16, (int)mw, 2);
+            mw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(m[j][3] * mi, h[3] << 16, (int)mw, 3);
+            sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][0] * si, h[0] & 0xFFFF0000u, (int)sw, 0);
+            sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][1] * si, h[1] & 0xFFFF0000u, (int)sw, 1);
+            sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][2] * si, h[2] & 0xFFFF0000u, (int)sw, 2);
+            sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][3] * si, h[3] & 0xFFFF0000u, (int)sw, 3);
         }
-        *reinterpret_cast<uint32_t*>(a.m8 + st + 128 * j) = top_bytes(mc);
-        *reinterpret_cast<uint32_t*>(a.s8 + st + 128 * j) = top_bytes(sc);
+        st<NT>(reinterpret_cast<uint32_t*>(a.m8 + at + 128 * j), mw);
+        st<NT>(reinterpret_cast<uint32_t*>(a.s8 + at + 128 * j), sw);
     }
 }
 
 // One run of 256 elements by half a wave: lane l (of 32) takes the elements
 // 4l.. and 128 + 4l.., so that every load and store of the half covers whole
 // 128-byte lines.
-template <int P, int G, bool S8, bool FULL>
+template <int P, int G, bool S8, bool FULL, bool NT>
 __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& ts, int64_t run, int l,
                                          float coef, float fa, float fb, float root_c, uint32_t key) {
     const int64_t sr = ts.state_run + run;
-    const int64_t st = sr * kRun + 4 * l;
+    const int64_t at = sr * kRun + 4 * l;
     const int64_t e0 = run * kRun + 4 * l;
     const int64_t rm = (ts.rem_run + run) * kRun + 4 * l;
     Raw<G> graw[2];
@@ -254,49 +286,62 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        graw[j] = load4<G, FULL>(ts.g_ptr, e0 + 128 * j, ts.numel);
-        praw[j] = load4<P, FULL>(ts.p_ptr, e0 + 128 * j, ts.numel);
-        if constexpr (P == DT_BF16) rem[j] = *reinterpret_cast<const u32x2*>(a.rem + rm + 128 * j);
+        graw[j] = load4<G, FULL, NT>(ts.g_ptr, e0 + 128 * j, ts.numel);
+        praw[j] = load4<P, FULL, NT>(ts.p_ptr, e0 + 128 * j, ts.numel);
+        if constexpr (P == DT_BF16) rem[j] = ld<NT>(reinterpret_cast<const u32x2*>(a.rem + rm + 128 * j));
         if constexpr (S8) {
-            mw[j] = *reinterpret_cast<const uint32_t*>(a.m8 + st + 128 * j);
-            sw[j] = *reinterpret_cast<const uint32_t*>(a.s8 + st + 128 * j);
+            mw[j] = ld<NT>(reinterpret_cast<const uint32_t*>(a.m8 + at + 128 * j));
+            sw[j] = ld<NT>(reinterpret_cast<const uint32_t*>(a.s8 + at + 128 * j));
         } else {
-            m[j] = *reinterpret_cast<const f32x4*>(a.m + st + 128 * j);
-            v[j] = *reinterpret_cast<const f32x4*>(a.v + st + 128 * j);
+            m[j] = ld<NT>(reinterpret_cast<const f32x4*>(a.m + at + 128 * j));
+            v[j] = ld<NT>(reinterpret_cast<const f32x4*>(a.v + at + 128 * j));
         }
     }
-    uint32_t tmin = 0xFFFFFFFFu, tmax = 0u;
+    uint32_t vmin = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const f32x4 g = widen4<G>(graw[j]);
+        f32x4 x = widen4<G>(graw[j]);
+        if (coef != 1.f)
+            for (int q = 0; q < 4; ++q) x[q] = x[q] * coef;
         if constexpr (S8) {
             m[j] = decode4(mw[j]);
             v[j] = decode4(sw[j]);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float x = g[q] * coef;
             if constexpr (S8) {
                 m[j][q] = m[j][q] * ms;
                 v[j][q] = v[j][q] * ss;
                 v[j][q] = v[j][q] * v[j][q];
             }
-            m[j][q] = m[j][q] * a.b1 + x * a.c1;
-            v[j][q] = v[j][q] * a.b2 + (x * x) * a.c2;
-            const uint32_t b = __float_as_uint(v[j][q]);
-            tmin = tmin < b - 1 ? tmin : b - 1;   // 0 counts as the largest
-            tmax = umax(tmax, b);
+            m[j][q] = m[j][q] * a.b1 + x[q] * a.c1;
+            v[j][q] = v[j][q] * a.b2 + (x[q] * x[q]) * a.c2;
+            vmin = umin(vmin, __float_as_uint(v[j][q]));
         }
     }
-    f32x4 root[2];
-    if (__any(tmin < kRootLow - 1 || tmax > kFinite)) {
+    f32x4 root[2], quo[2];
+    uint32_t smax = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            root[j][q] = near_root(v[j][q]);
+            smax = umax(smax, __float_as_uint(root[j][q]));
+        }
+    if (__any(vmin < kRootLow || smax > kFinite)) {
+        // zeros, tiny second moments and those that are not finite
+        smax = 0;
         for (int j = 0; j < 2; ++j)
-            for (int q = 0; q < 4; ++q) root[j][q] = sqrtf(v[j][q]);
+            for (int q = 0; q < 4; ++q) {
+                root[j][q] = sqrtf(v[j][q]);
+                smax = umax(smax, __float_as_uint(root[j][q]));
+                quo[j][q] = m[j][q] / (root[j][q] * root_c + a.eps);
+            }
     } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) root[j][q] = near_root(v[j][q]);
+            for (int q = 0; q < 4; ++q) quo[j][q] = quotient(m[j][q], root[j][q] * root_c + a.eps);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -315,10 +360,7 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
             w = praw[j].w;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float d = root[j][q] * root_c + a.eps;
-            w[q] = w[q] - (w[q] * fa + quotient(m[j][q], d) * fb);
-        }
+        for (int q = 0; q < 4; ++q) w[q] = w[q] - (w[q] * fa + quo[j][q] * fb);
         if constexpr (P == DT_BF16) {
             // the nearest bf16 (ties away from zero) is the upper half of bits +
             // 2^15, and what is left, as a signed number, is the lower half of
@@ -330,29 +372,36 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
                 out.w[k] = __builtin_amdgcn_perm(b[2 * k + 1] + 0x8000u, b[2 * k] + 0x8000u, 0x07060302u);
                 left[k] = __builtin_amdgcn_perm(b[2 * k + 1], b[2 * k], 0x05040100u);
             }
-            *reinterpret_cast<u32x2*>(a.rem + rm + 128 * j) = left;
+            st<NT>(reinterpret_cast<u32x2*>(a.rem + rm + 128 * j), left);
         } else {
             out.w = w;
         }
-        store4<P, FULL>(ts.p_ptr, e0 + 128 * j, ts.numel, out);
+        store4<P, FULL, NT>(ts.p_ptr, e0 + 128 * j, ts.numel, out);
         if constexpr (!S8) {
-            *reinterpret_cast<f32x4*>(a.m + st + 128 * j) = m[j];
-            *reinterpret_cast<f32x4*>(a.v + st + 128 * j) = v[j];
+            st<NT>(reinterpret_cast<f32x4*>(a.m + at + 128 * j), m[j]);
+            st<NT>(reinterpret_cast<f32x4*>(a.v + at + 128 * j), v[j]);
         }
     }
     if constexpr (S8) {
-        uint32_t mmax = 0, smax = 0;
+        // the largest magnitude of m as the largest signed and the largest
+        // unsigned of its bits: positive and negative values, NaN above all
+        int mpos = 0;
+        uint32_t mneg = 0;
+        float mlow = __builtin_inff(), slow = __builtin_inff();
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                mmax = umax(mmax, __float_as_uint(m[j][q]) & 0x7FFFFFFFu);
-                smax = umax(smax, __float_as_uint(root[j][q]) & 0x7FFFFFFFu);
+                const int b = (int)__float_as_uint(m[j][q]);
+                mpos = mpos > b ? mpos : b;
+                mneg = umax(mneg, (uint32_t)b);
+                mlow = fminf(mlow, fabsf(m[j][q]));
+                slow = fminf(slow, root[j][q]);
             }
-        mmax = half_max(mmax);
-        smax = half_max(smax);
-        const bool any = __any(umax(mmax, smax) > kFinite);
-        if (any) {   // the scales are those of the finite values
+        uint32_t mmax = umax((uint32_t)mpos, mneg & 0x7FFFFFFFu);
+        uint32_t top = half_max2(mmax, smax);
+        const bool odd = __any(top > kFinite);
+        if (odd) {   // the scales are those of the finite values
             mmax = smax = 0;
             for (int j = 0; j < 2; ++j)
                 for (int q = 0; q < 4; ++q) {
@@ -361,26 +410,31 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
                     mmax = umax(mmax, mb <= kFinite ? mb : 0u);
                     smax = umax(smax, sb <= kFinite ? sb : 0u);
                 }
-            mmax = half_max(mmax);
-            smax = half_max(smax);
+            top = half_max2(mmax, smax);
         }
-        float mi, si;
-        run_scale(mmax, ms, mi);
-        run_scale(smax, ss, si);
-        if (l == 0) {
-            a.m_scale[sr] = ms;
-            a.s_scale[sr] = ss;
-        }
-        key += (uint32_t)((uint64_t)e0 >> 32) * 0x85157AF5u;
-        if (any) encode_run<true>(a, m, root, mi, si, key, (uint32_t)e0, st);
-        else encode_run<false>(a, m, root, mi, si, key, (uint32_t)e0, st);
+        // the first row works on m, the second on the root
+        float scale, inv, mi, si;
+        run_scale(top, scale, inv);
+        half_both(inv, mi, si);
+        if ((l & 15) == 0) (l == 0 ? a.m_scale : a.s_scale)[sr] = scale;
+        uint32_t start = (key + (uint32_t)((uint64_t)e0 >> 32) * 0x85157AF5u) ^ (uint32_t)e0;
+        start ^= start >> 16;
+        if (__any(mlow * mi < 0x1p-6f || slow * si < 0x1p-6f) || odd)
+            encode_run<true, NT>(a, m, root, mi, si, start, at);
+        else
+            encode_run<false, NT>(a, m, root, mi, si, start, at);
     }
 }
 
 // One step of the elements of this wave's tiles.
-template <int P, int G, bool S8>
+template <int P, int G, bool S8, bool NT>
 __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
-    const AdamwClock clk = a.clocks[blockIdx.x];
+    // field by field: a copy of the whole struct, its padding included, went
+    // through LDS and cost 14 us at 256 workgroups
+    AdamwClock* clock = a.clocks + blockIdx.x;
+    const int64_t t = clock->t;
+    const double b1t = clock->b1t, b2t = clock->b2t, inv1 = clock->inv1;
+    const float root_c = clock->inv_root2;
     float coef = 1.f;
     if (a.clip) {
         if (a.clip->nonfinite) return;   // the same for every workgroup: nothing changes
@@ -389,33 +443,32 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
     const int lane = threadIdx.x & 63, l = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-    const uint32_t key0 = mix32(a.seed_mixed + (uint32_t)(clk.t + 1));
-    for (int i = wave; i < a.ntiles; i += gridDim.x * 4) {
-        const AdamwTile tl = a.tiles[i];
+    const uint32_t key0 = mix32(a.seed_mixed + (uint32_t)(t + 1));
+    if (wave < a.ntiles) {
+        const AdamwTile tl = a.tiles[wave];
         const AdamwTensor ts = a.tensors[tl.tensor];
-        if (!ts.g_ptr) continue;
         const float fa = (float)(lr * ts.lr_scale * ts.weight_decay);
-        const float fb = (float)(lr * ts.lr_scale * clk.inv1);
+        const float fb = (float)(lr * ts.lr_scale * inv1);
         const uint32_t key = mix32(key0 + (uint32_t)ts.id);
         // two runs at a time, one to each half; an odd last run is taken by
         // both halves' lanes together with a run that has no elements
-        for (int k = 0; k < tl.nruns; k += 2) {
+        const int nruns = ts.g_ptr ? tl.nruns : 0;
+        for (int k = 0; k < nruns; k += 2) {
             const int64_t run = tl.run0 + k + (lane >> 5);
             if ((tl.run0 + k + 2) * kRun <= ts.numel)
-                step_run<P, G, S8, true>(a, ts, run, l, coef, fa, fb, clk.inv_root2, key);
+                step_run<P, G, S8, true, NT>(a, ts, run, l, coef, fa, fb, root_c, key);
             else if (run * kRun < ts.numel)
-                step_run<P, G, S8, false>(a, ts, run, l, coef, fa, fb, clk.inv_root2, key);
+                step_run<P, G, S8, false, false>(a, ts, run, l, coef, fa, fb, root_c, key);
         }
     }
     __syncthreads();   // every wave has read the clock
     if (threadIdx.x == 0) {
-        AdamwClock n = clk;
-        n.t += 1;
-        n.b1t *= a.beta1;
-        n.b2t *= a.beta2;
-        n.inv1 = 1.0 / (1.0 - n.b1t);
-        n.inv_root2 = (float)(1.0 / sqrt(1.0 - n.b2t));
-        a.clocks[blockIdx.x] = n;
+        const double n1 = b1t * a.beta1, n2 = b2t * a.beta2;
+        clock->t = t + 1;
+        clock->b1t = n1;
+        clock->b2t = n2;
+        clock->inv1 = 1.0 / (1.0 - n1);
+        clock->inv_root2 = (float)(1.0 / sqrt(1.0 - n2));
     }
 }
 
@@ -544,8 +597,13 @@ __global__ __launch_bounds__(256) void k_clip(NormArgs a) {
 template <int P, int G>
 hipError_t go(bool bits8, const AdamwArgs& a, hipStream_t s) {
     const dim3 grid(adamw_grid(a.ntiles)), block(256);
-    if (bits8) hipLaunchKernelGGL((k_adamw<P, G, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_adamw<P, G, false>), grid, block, 0, s, a);
+    if (bits8) {
+        if (a.stream_past) hipLaunchKernelGGL((k_adamw<P, G, true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_adamw<P, G, true, false>), grid, block, 0, s, a);
+    } else {
+        if (a.stream_past) hipLaunchKernelGGL((k_adamw<P, G, false, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_adamw<P, G, false, false>), grid, block, 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -558,9 +616,9 @@ hipError_t go_grad(int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Eight workgroups on each of the 256 CUs at most, four tiles (one per wave)
-// to a workgroup.
-int adamw_grid(int64_t ntiles) { return (int)(ntiles < 8192 ? (ntiles + 3) / 4 : 2048); }
+// Four tiles, one per wave, to a workgroup.
+int adamw_grid(int64_t ntiles) { return (int)((ntiles + 3) / 4); }
+// At most four workgroups on each of the 256 CUs.
 int norm_grid(int64_t ntiles) { return (int)(ntiles < 4096 ? (ntiles + 3) / 4 + (ntiles == 0) : 1024); }
 
 hipError_t launch_adamw(int param, int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {

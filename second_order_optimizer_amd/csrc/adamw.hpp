@@ -60,6 +60,7 @@ struct AdamwArgs {
     float b1, c1, b2, c2, eps;   // beta1, 1 - beta1, beta2, 1 - beta2, eps
     uint32_t seed_mixed;
     int32_t ntiles;
+    int32_t stream_past;         // the step touches more than the caches hold
     float *m, *v;                // fp32 moments
     unsigned char *m8, *s8;      // 8-bit moments: e4m3 of m and sqrt(v)
     float *m_scale, *s_scale;
@@ -93,14 +94,14 @@ struct NormArgs {
 };
 
 // 32 bits mixed by two rounds of shift-xor and odd multiplication.
-__host__ __device__ inline uint32_t mix32(uint32_t x) {
-    x ^= x >> 16;
+__host__ __device__ inline uint32_t mix32_rest(uint32_t x) {   // after the first shift-xor
     x *= 0xFD63ED5Bu;
     x ^= x >> 15;
     x *= 0x7BC73A83u;
     x ^= x >> 16;
     return x;
 }
+__host__ __device__ inline uint32_t mix32(uint32_t x) { return mix32_rest(x ^ (x >> 16)); }
 
 int adamw_grid(int64_t ntiles);
 int norm_grid(int64_t ntiles);
