@@ -59,15 +59,18 @@ class _Bound:
         self.device = dev
         self._types = (torch.float32, torch.bfloat16, torch.float16)
 
+        # the current stream of a device as a number, without a Stream object
+        self._stream = torch._C._cuda_getCurrentRawStream
+        self._current = torch.cuda.current_device
+
     def _call(self, fn, *args):
         """fn(handle, *args, stream) with the handle's device current."""
-        cuda = self.torch.cuda
-        stream = cuda.current_stream(self.device).cuda_stream
-        if cuda.current_device() == self.device.index:
-            rc = fn(self.h, *args, stream)
+        index = self.device.index
+        if self._current() == index:
+            rc = fn(self.h, *args, self._stream(index))
         else:
-            with cuda.device(self.device):
-                rc = fn(self.h, *args, stream)
+            with self.torch.cuda.device(index):
+                rc = fn(self.h, *args, self._stream(index))
         if rc:
             _check(rc, fn.__name__)
 

@@ -70,6 +70,8 @@ struct shampoo_adamw_s {
 struct shampoo_gradnorm_s {
     std::vector<NormTensor> table;
     std::vector<NormTile> tiles;
+    int pieces = 1;           // pieces of a tile
+    int64_t grad_bytes = 0;
     int64_t off_table = 0, off_tiles = 0, off_partials = 0, off_ticket = 0, off_record = 0;
     size_t total = 0;
     unsigned char* arena = nullptr;
@@ -165,6 +167,7 @@ NormArgs norm_args(shampoo_gradnorm_s* h) {
     a.tensors = reinterpret_cast<const NormTensor*>(h->arena + h->off_table);
     a.tiles = reinterpret_cast<const NormTile*>(h->arena + h->off_tiles);
     a.ntiles = (int32_t)h->tiles.size();
+    a.pieces = h->pieces;
     a.partials = reinterpret_cast<double*>(h->arena + h->off_partials);
     a.ticket = reinterpret_cast<int32_t*>(h->arena + h->off_ticket);
     a.record = reinterpret_cast<ClipRecord*>(h->arena + h->off_record);
@@ -335,18 +338,23 @@ int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
         if (d.numel < 0 || d.reserved != 0 || d.dtype < SHAMPOO_F32 || d.dtype > SHAMPOO_F16)
             return SHAMPOO_E_ARG;
         if (d.numel > kMaxNumel) return SHAMPOO_E_UNSUPPORTED;
-        tiles += d.numel / kNormTile + 1;
+        tiles += d.numel / kNormPiece + 1;
         if (tiles > kMaxTiles) return SHAMPOO_E_UNSUPPORTED;
     }
     shampoo_gradnorm_s* h = new (std::nothrow) shampoo_gradnorm_s();
     if (!h) return SHAMPOO_E_NOMEM;
+    // twice the work for one reading of the tables once every wave has several
+    // (302M bf16 elements: 103 us, 108 with four)
+    h->pieces = tiles >= 8 * 8192 ? 2 : 1;
     try {
+        const int64_t per_tile = (int64_t)h->pieces * kNormPiece;
         for (int i = 0; i < n_tensors; ++i) {
             NormTensor t{};
             t.numel = tensors[i].numel;
             t.dtype = tensors[i].dtype;
             h->table.push_back(t);
-            for (int64_t k = 0; k < t.numel; k += kNormTile) h->tiles.push_back({i, 0, k});
+            h->grad_bytes += t.numel * (int64_t)dtype_bytes(t.dtype);
+            for (int64_t k = 0; k < t.numel; k += per_tile) h->tiles.push_back({i, 0, k});
         }
     } catch (const std::bad_alloc&) {
         delete h;
@@ -430,6 +438,9 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
         return SHAMPOO_E_ARG;
     if (!h->bound || !h->grads_bound || !on_device(h->device)) return SHAMPOO_E_STATE;
     NormArgs a = norm_args(h);
+    // gradients that fit the last-level cache are found there by the step that
+    // follows (302M bf16 elements: 93 us past the caches, 103 through them)
+    a.stream_past = h->grad_bytes > kCacheBytes;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
     return status_of(launch_norm(a, static_cast<hipStream_t>(stream)));
@@ -438,6 +449,7 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream) {
     if (!h) return SHAMPOO_E_ARG;
     if (!h->bound || !h->grads_bound || !on_device(h->device)) return SHAMPOO_E_STATE;
+    if (h->tiles.empty()) return SHAMPOO_OK;
     return status_of(launch_clip(norm_args(h), static_cast<hipStream_t>(stream)));
 }
 

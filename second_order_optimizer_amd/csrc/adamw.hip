@@ -499,53 +499,132 @@ __device__ __forceinline__ double wave_sum_d(double v) {
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
     return v;
 }
+// The sum over a workgroup of kNormWaves waves, to every lane.
 __device__ __forceinline__ double group_sum(double v, double* red) {
     v = wave_sum_d(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    const int l = threadIdx.x & 63;
+    return wave_sum_d(l < kNormWaves ? red[l] : 0.0);
+}
+
+// 16 bytes of a gradient per lane and load: a wave reads a piece of kNormPiece
+// elements with all its loads in flight.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+template <int DT> struct Piece {
+    static constexpr int kPer = DT == DT_F32 ? 4 : 8;          // elements of a load
+    static constexpr int kLoads = kNormPiece / 64 / kPer;
+    u32x4 w[kLoads];
+};
+
+template <int DT, bool NT>
+__device__ __forceinline__ void load_piece(Piece<DT>& r, uint64_t g, int64_t first, int64_t numel, int lane) {
+    typedef typename Elem<DT>::type T;
+    constexpr int kPer = Piece<DT>::kPer;
+    if (first + kNormPiece <= numel) {
+#pragma unroll
+        for (int k = 0; k < Piece<DT>::kLoads; ++k)
+            r.w[k] = ld<NT>(gptr<const u32x4h>(g + (uint64_t)(first + (k * 64 + lane) * kPer) * sizeof(T)));
+        return;
+    }
+    for (int k = 0; k < Piece<DT>::kLoads; ++k) {
+        const int64_t e = first + (k * 64 + lane) * kPer;
+        const uint64_t at = g + (uint64_t)e * sizeof(T);
+        if (e + kPer <= numel) {
+            r.w[k] = *gptr<const u32x4h>(at);
+        } else {
+            r.w[k] = u32x4{0, 0, 0, 0};
+            for (int q = 0; q < kPer; ++q)
+                if (e + q < numel) {
+                    if constexpr (DT == DT_F32) r.w[k][q] = gptr<const uint32_t>(at)[q];
+                    else r.w[k][q >> 1] |= (uint32_t)gptr<const unsigned short>(at)[q] << (16 * (q & 1));
+                }
+        }
+    }
 }
 
 template <int DT>
-__device__ __forceinline__ double tile_squares(uint64_t g, int64_t first, int64_t numel, int lane) {
+__device__ __forceinline__ double piece_squares(const Piece<DT>& r) {
     double s[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < kNormTile / 256; ++k) {
-        const f32x4 x = widen4<DT>(load4<DT, false>(g, first + k * 256 + lane * 4, numel));
-        for (int q = 0; q < 4; ++q) s[q] += (double)x[q] * (double)x[q];
-    }
+    for (int k = 0; k < Piece<DT>::kLoads; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (DT == DT_F32) {
+                const double x = (double)__uint_as_float(r.w[k][q]);
+                s[q] = __builtin_fma(x, x, s[q]);
+            } else {
+                const Raw<DT> two{u32x2{r.w[k][q], 0u}};
+                const f32x4 f = widen4<DT>(two);
+                const double x = (double)f[0], y = (double)f[1];
+                s[q] = __builtin_fma(x, x, s[q]);
+                s[q] = __builtin_fma(y, y, s[q]);
+            }
+        }
     return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <int DT, bool NT>
+__device__ __forceinline__ double tile_squares(const NormTensor& ts, int64_t first, int pieces, int lane) {
+    double acc = 0.0;
+    for (int p = 0; p < pieces; ++p) {
+        const int64_t e = first + (int64_t)p * kNormPiece;
+        if (e >= ts.numel) break;
+        Piece<DT> r;
+        load_piece<DT, NT>(r, ts.g_ptr, e, ts.numel, lane);
+        acc += piece_squares<DT>(r);
+    }
+    return acc;
 }
 
 // Sum of the squares of every gradient in fp64 (the squares of fp32 values
 // are exact in it, none overflows), in an order that the plan fixes: each
 // wave over its tiles, each workgroup over its waves, the last workgroup to
 // finish over the workgroups' sums.
-__global__ __launch_bounds__(256) void k_norm(NormArgs a) {
-    __shared__ double red[4];
+template <bool NT>
+__global__ __launch_bounds__(64 * kNormWaves) void k_norm(NormArgs a) {
+    __shared__ double red[kNormWaves];
     __shared__ int last;
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * kNormWaves + (threadIdx.x >> 6));
     double acc = 0.0;
-    for (int i = wave; i < a.ntiles; i += gridDim.x * 4) {
-        const NormTile tl = a.tiles[i];
-        const NormTensor ts = a.tensors[tl.tensor];
-        if (!ts.g_ptr) continue;
-        if (ts.dtype == DT_F32) acc += tile_squares<DT_F32>(ts.g_ptr, tl.first, ts.numel, lane);
-        else if (ts.dtype == DT_BF16) acc += tile_squares<DT_BF16>(ts.g_ptr, tl.first, ts.numel, lane);
-        else acc += tile_squares<DT_F16>(ts.g_ptr, tl.first, ts.numel, lane);
+    // the tables are read ahead: the tile after next and the next one's tensor
+    // while a tile's gradients arrive
+    const int stride = gridDim.x * kNormWaves, end = a.ntiles - 1;
+    if (wave <= end) {
+        NormTile tl = a.tiles[wave];
+        NormTile next = a.tiles[wave + stride < end ? wave + stride : end];
+        NormTensor ts = a.tensors[tl.tensor];
+        for (int i = wave; i <= end; i += stride) {
+            const NormTile later = a.tiles[i + 2 * stride < end ? i + 2 * stride : end];
+            const NormTensor tn = a.tensors[next.tensor];
+            if (ts.g_ptr) {
+                if (ts.dtype == DT_F32) acc += tile_squares<DT_F32, NT>(ts, tl.first, a.pieces, lane);
+                else if (ts.dtype == DT_BF16) acc += tile_squares<DT_BF16, NT>(ts, tl.first, a.pieces, lane);
+                else acc += tile_squares<DT_F16, NT>(ts, tl.first, a.pieces, lane);
+            }
+            tl = next;
+            next = later;
+            ts = tn;
+        }
     }
     const double sum = group_sum(acc, red);
     if (threadIdx.x == 0) {
+        // The sum is written through to where every XCD reads it, and is there
+        // before this workgroup counts itself as done.  A release at agent
+        // scope would also write the whole L2 back, 60 ns a workgroup one
+        // after another.
         __hip_atomic_store(a.partials + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                (int)gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
     double t = 0.0;
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += 256)
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 64 * kNormWaves)
         t += __hip_atomic_load(a.partials + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     t = group_sum(t, red);
     if (threadIdx.x == 0) {
@@ -562,16 +641,28 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a) {
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void tile_clip(const NormTensor& ts, int64_t first, int lane, float coef,
-                                          bool zero) {
+template <int DT, bool FULL>
+__device__ __forceinline__ void piece_clip(const NormTensor& ts, int64_t first, int lane, float coef, bool zero) {
+    Raw<DT> raw[kNormPiece / 256];
 #pragma unroll
-    for (int k = 0; k < kNormTile / 256; ++k) {
-        const int64_t e = first + k * 256 + lane * 4;
-        const f32x4 x = widen4<DT>(load4<DT, false>(ts.g_ptr, e, ts.numel));
+    for (int k = 0; k < kNormPiece / 256; ++k)
+        raw[k] = load4<DT, FULL>(ts.g_ptr, first + k * 256 + lane * 4, ts.numel);
+#pragma unroll
+    for (int k = 0; k < kNormPiece / 256; ++k) {
+        const f32x4 x = widen4<DT>(raw[k]);
         Raw<DT_F32> y;
         for (int q = 0; q < 4; ++q) y.w[q] = zero ? 0.f : x[q] * coef;
-        store4<DT_F32, false>(ts.out_ptr, e, ts.numel, y);
+        store4<DT_F32, FULL>(ts.out_ptr, first + k * 256 + lane * 4, ts.numel, y);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void tile_clip(const NormTensor& ts, int64_t first, int pieces, int lane, float coef,
+                                          bool zero) {
+    for (int p = 0; p < pieces; ++p) {
+        const int64_t e = first + (int64_t)p * kNormPiece;
+        if (e >= ts.numel) break;
+        if (e + kNormPiece <= ts.numel) piece_clip<DT, true>(ts, e, lane, coef, zero);
+        else piece_clip<DT, false>(ts, e, lane, coef, zero);
     }
 }
 
@@ -580,18 +671,16 @@ __device__ __forceinline__ void tile_clip(const NormTensor& ts, int64_t first, i
 __global__ __launch_bounds__(256) void k_clip(NormArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-    const ClipRecord r = *a.record;
-    for (int i = wave; i < a.ntiles; i += gridDim.x * 4) {
-        const NormTile tl = a.tiles[i];
-        const NormTensor ts = a.tensors[tl.tensor];
-        if (!ts.g_ptr || !ts.out_ptr) continue;
-        // in place and nothing to clip: the gradient stands
-        if (ts.out_ptr == ts.g_ptr && r.coef == 1.f) continue;
-        const bool zero = r.nonfinite != 0;
-        if (ts.dtype == DT_F32) tile_clip<DT_F32>(ts, tl.first, lane, r.coef, zero);
-        else if (ts.dtype == DT_BF16) tile_clip<DT_BF16>(ts, tl.first, lane, r.coef, zero);
-        else tile_clip<DT_F16>(ts, tl.first, lane, r.coef, zero);
-    }
+    if (wave >= a.ntiles) return;
+    const float coef = a.record->coef;
+    const bool zero = a.record->nonfinite != 0;
+    const NormTile tl = a.tiles[wave];
+    const NormTensor ts = a.tensors[tl.tensor];
+    // nothing asked for, or in place and nothing to clip
+    if (!ts.g_ptr || !ts.out_ptr || (ts.out_ptr == ts.g_ptr && coef == 1.f)) return;
+    if (ts.dtype == DT_F32) tile_clip<DT_F32>(ts, tl.first, a.pieces, lane, coef, zero);
+    else if (ts.dtype == DT_BF16) tile_clip<DT_BF16>(ts, tl.first, a.pieces, lane, coef, zero);
+    else tile_clip<DT_F16>(ts, tl.first, a.pieces, lane, coef, zero);
 }
 
 template <int P, int G>
@@ -618,8 +707,12 @@ hipError_t go_grad(int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {
 
 // Four tiles, one per wave, to a workgroup.
 int adamw_grid(int64_t ntiles) { return (int)((ntiles + 3) / 4); }
-// At most four workgroups on each of the 256 CUs.
-int norm_grid(int64_t ntiles) { return (int)(ntiles < 4096 ? (ntiles + 3) / 4 + (ntiles == 0) : 1024); }
+// At most two workgroups of eight waves on each of the 256 CUs (302M bf16
+// elements: 103 us; with 16 waves 108, with 1024 workgroups of four 105): they
+// are counted one after another, 12 ns each.
+int norm_grid(int64_t ntiles) {
+    return (int)(ntiles < 512 * kNormWaves ? (ntiles + kNormWaves - 1) / kNormWaves + (ntiles == 0) : 512);
+}
 
 hipError_t launch_adamw(int param, int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {
     return param == DT_F32 ? go_grad<DT_F32>(grad, bits8, a, s)
@@ -644,12 +737,14 @@ hipError_t launch_norm_bind(NormTensor* tensors, int first, int n, const PtrBatc
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_norm, dim3(norm_grid(a.ntiles)), dim3(256), 0, s, a);
+    const dim3 grid(norm_grid(a.ntiles)), block(64 * kNormWaves);
+    if (a.stream_past) hipLaunchKernelGGL(k_norm<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_norm<false>, grid, block, 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_clip(const NormArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_clip, dim3(norm_grid(a.ntiles)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_clip, dim3((a.ntiles + 3) / 4), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -81,14 +81,16 @@ struct NormTile {
     int32_t tensor, pad_;
     int64_t first;            // first element of the tile
 };
-constexpr int kNormTile = 2048;   // elements of one tile, the work of one wave
+constexpr int kNormWaves = 8;    // waves of a workgroup of the norm
+constexpr int kNormPiece = 1024;  // elements that a wave has in flight together; a tile is some
 
 struct NormArgs {
     const NormTensor* tensors;
     const NormTile* tiles;
-    int32_t ntiles, pad_;
+    int32_t ntiles, pieces;   // pieces of a tile
     double* partials;         // one per workgroup
     int32_t* ticket;
+    int32_t stream_past, pad_; // the gradients are more than the caches hold
     ClipRecord* record;
     double max_norm, grad_scale;
 };
