@@ -431,6 +431,7 @@ const char* shampoo_strerror(int status);
  * count matters) and may start at any element; sizes of 0 are allowed.  The
  * calls below other than *_bind_state allocate nothing, upload nothing and
  * never wait, so they can be captured into a graph; replays count steps on.
+ * Tensors, state and records stay alive until the work that uses them is done.
  * Calls need the device current that was current at *_bind_state
  * (SHAMPOO_E_STATE otherwise).  Results do not depend on how the work was
  * distributed: they are bit for bit repeatable. */
@@ -448,7 +449,8 @@ typedef struct {
 
 /* What shampoo_gradnorm_compute leaves on the device. */
 typedef struct {
-    float norm;          /* n = grad_scale sqrt(sum of all g^2), summed in fp64          */
+    float norm;          /* n = grad_scale sqrt(sum of all g^2), summed in fp64 (infinite
+                            past the range of fp32)                                      */
     float coef;          /* grad_scale min(1, max_norm / n): the factor of a clipped
                             gradient; 0 when n is not finite                             */
     int32_t nonfinite;   /* 1: n is not finite (some gradient is infinite or NaN)        */
@@ -469,10 +471,11 @@ int shampoo_gradnorm_bind_state(shampoo_gradnorm_t* h, void* dev_state, size_t b
 /* The gradients' device addresses from now on (until bound again; the calls
  * that follow on `stream` read them).  A null gradient counts as absent.
  * outs: NULL, or for each tensor null or the fp32 tensor that
- * shampoo_gradnorm_clip_into fills: the gradient itself where that is fp32,
- * otherwise memory that overlaps no gradient.  Errors: SHAMPOO_E_ARG (null
- * grads, an address not aligned to its element, an output in place of a
- * gradient that is not fp32), SHAMPOO_E_STATE, SHAMPOO_E_HIP. */
+ * shampoo_gradnorm_clip_into fills: its own gradient where that is fp32,
+ * otherwise memory that overlaps no gradient and no other output.  Errors:
+ * SHAMPOO_E_ARG (null grads, an address not aligned to its element, outputs
+ * that overlap each other or a gradient otherwise), SHAMPOO_E_STATE,
+ * SHAMPOO_E_HIP, SHAMPOO_E_NOMEM. */
 int shampoo_gradnorm_bind_grads(shampoo_gradnorm_t* h, const void* const* grads, float* const* outs,
                                 void* stream);
 /* Norm and clip coefficient of the bound gradients into the device record.
@@ -525,9 +528,10 @@ typedef struct {
 } shampoo_adamw_layout;
 
 /* Plan for n_tensors tensors.  Host only.  Errors: SHAMPOO_E_ARG (null,
- * n_tensors < 1, numel < 0, a beta outside [0, 1), eps out of range, weight_decay or lr_scale negative or not finite, unknown types,
- * state_bits not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16
- * weights, numel above 2^38), SHAMPOO_E_NOMEM. */
+ * n_tensors < 1, numel < 0, a beta outside [0, 1), eps out of range,
+ * weight_decay or lr_scale negative or not finite, unknown types, state_bits
+ * not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16 weights, numel
+ * above 2^38), SHAMPOO_E_NOMEM. */
 int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,
                          const shampoo_adamw_tensor* tensors, shampoo_adamw_t** out);
 int shampoo_adamw_get_layout(const shampoo_adamw_t* h, shampoo_adamw_layout* out);
@@ -541,10 +545,10 @@ int shampoo_adamw_tensor_runs(const shampoo_adamw_t* h, int32_t tensor, int64_t*
 int shampoo_adamw_bind_state(shampoo_adamw_t* h, void* dev_state, size_t bytes, void* stream);
 /* The tensors' device addresses from now on, until bound again; params or
  * grads may be NULL to keep those bound before.  A null gradient (none this
- * step) leaves its tensor's weights and moments as they are.  Gradients and
- * weights must not overlap each other.  Errors: SHAMPOO_E_ARG (both NULL, a
- * null weight, an address not aligned to its element), SHAMPOO_E_STATE,
- * SHAMPOO_E_HIP. */
+ * step) leaves its tensor's weights and moments as they are.  Gradients must
+ * not overlap weights.  Errors: SHAMPOO_E_ARG (both NULL, a null weight, an
+ * address not aligned to its element, weights that overlap), SHAMPOO_E_STATE,
+ * SHAMPOO_E_HIP, SHAMPOO_E_NOMEM. */
 int shampoo_adamw_bind_tensors(shampoo_adamw_t* h, void* const* params, const void* const* grads,
                                void* stream);
 /* Set the number of steps done (t >= 0), e.g. after restoring the moments. */

@@ -13,9 +13,11 @@ bits, and the global gradient norm whose clip coefficient it reads.
         opt.step(lr=1e-3, clip=norm)
 
 Beside Shampoo, GradNorm takes the gradients of both optimizers and
-``clip_into`` writes the fp32 ones that Shampoo.step takes.  Nothing here
-waits for the GPU or copies to it after ``__init__``.  It raises if the library
-has not been built -- there is no fallback.
+``clip_into`` writes the fp32 ones that Shampoo.step takes.  ``bind``,
+``compute``, ``clip_into`` and ``step`` neither wait for the GPU nor copy to it,
+and can be captured into a graph; what is bound or captured stays alive, and is
+used by one stream at a time.  It raises if the library has not been built --
+there is no fallback.
 """
 from __future__ import annotations
 
@@ -56,6 +58,8 @@ class _Bound:
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
+        if dev.type != "cuda":
+            raise ValueError(f"no kernels for {dev}")
         self.device = dev
         self._types = (torch.float32, torch.bfloat16, torch.float16)
 
@@ -228,3 +232,18 @@ class AdamW(_Bound):
         if lay.runs_rem:
             out["rem"] = self._view(lay.off_rem, lay.runs_rem * RUN, t.int16)
         return out
+
+    def state_dict(self) -> Dict[str, object]:
+        """Copies of the moments and remainders, and the number of steps done
+        (waits for the GPU)."""
+        return {"t": int(self.t), **{k: x.clone() for k, x in self.state_tensors().items()}}
+
+    def load_state_dict(self, saved: Dict[str, object]):
+        """Restore what ``state_dict`` of a handle with the same tensors gave."""
+        held = self.state_tensors()
+        if set(saved) != {"t", *held} or any(saved[k].shape != x.shape or saved[k].dtype != x.dtype
+                                             for k, x in held.items()):
+            raise ValueError("the state is of other tensors")
+        for k, x in held.items():
+            x.copy_(saved[k])
+        self.set_step(saved["t"])

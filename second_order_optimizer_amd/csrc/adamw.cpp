@@ -29,6 +29,9 @@ constexpr int64_t kMaxNumel = (int64_t)1 << 38;    // runs of a tensor stay belo
 // turn of 16M fp32 elements: 80 us, 92 through the caches; of 4M: 22 us, 19
 // through them).  Of the 256 MiB last-level cache a program leaves a step part.
 constexpr int64_t kCacheBytes = (int64_t)96 << 20;
+// Gradients up to this stay there between their norm and the step that reads
+// them again (60M bf16 elements, norm and 8-bit step: 168 us, 174 past it).
+constexpr int64_t kGradCacheBytes = (int64_t)192 << 20;
 constexpr double kMinEps = 0x1p-100;               // sqrt(v) c + eps is a normal number
 constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 
@@ -41,6 +44,20 @@ size_t dtype_bytes(int dt) { return dt == SHAMPOO_F32 ? 4 : 2; }
 bool on_device(int device) {
     int d = -1;
     return hipGetDevice(&d) == hipSuccess && d == device;
+}
+
+// Whether any two of these address ranges share a byte.
+struct Span {
+    uint64_t begin, end;
+};
+bool overlap(std::vector<Span>& v) {
+    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    for (size_t i = 1; i < v.size(); ++i)
+        if (v[i].begin < v[i - 1].end) return true;
+    return false;
+}
+void add_span(std::vector<Span>& v, const void* p, int64_t bytes) {
+    if (p && bytes > 0) v.push_back({reinterpret_cast<uint64_t>(p), reinterpret_cast<uint64_t>(p) + (uint64_t)bytes});
 }
 
 // The launch of the tensors that share one kernel.
@@ -72,7 +89,7 @@ struct shampoo_gradnorm_s {
     std::vector<NormTile> tiles;
     int pieces = 1;           // pieces of a tile
     int64_t grad_bytes = 0;
-    int64_t off_table = 0, off_tiles = 0, off_partials = 0, off_ticket = 0, off_record = 0;
+    int64_t off_table = 0, off_tiles = 0, off_partials = 0, off_tickets = 0, off_record = 0;
     size_t total = 0;
     unsigned char* arena = nullptr;
     bool bound = false, grads_bound = false;
@@ -94,11 +111,12 @@ AdamwClock clock_at(const shampoo_adamw_config& c, int64_t t) {
 void plan_adamw(shampoo_adamw_s* h) {
     int64_t runs[2] = {0, 0}, rem_runs = 0, total_runs = 0;
     for (const auto& d : h->desc) total_runs += runs_of(d.numel);
-    // A wave takes two runs at a time, one to each half.  Tiles of two spread
-    // small plans over the chip (1M fp32 elements: 6.3 us, 7.4 with tiles of
-    // four); tiles of four read half the tables once there are four waves for
-    // each SIMD (200M fp32 elements: 915 us, 944 with two, 1043 with eight).
-    const int64_t per_tile = total_runs >= 4 * 4096 ? 4 : 2;
+    // A wave takes two runs at a time, one to each half, and one such pair is a
+    // tile.  With 8-bit moments, where a pair is half the bytes, tiles of two
+    // pairs once there are four waves for each SIMD (302M bf16 elements: 700
+    // us, 721 with one pair; 1M: 6.3 and 5.5 us.  fp32 moments, 302M fp32
+    // elements: 1428 us with one pair, 1487 with two).
+    const int64_t wide = total_runs >= 4 * 4096 ? 4 : 2;
     for (size_t i = 0; i < h->desc.size(); ++i) {
         const auto& d = h->desc[i];
         AdamwTensor t{};
@@ -125,6 +143,7 @@ void plan_adamw(shampoo_adamw_s* h) {
             g->grad = d.grad_type;
             g->bits8 = d.state_bits == 8;
         }
+        const int64_t per_tile = d.state_bits == 8 ? wide : 2;
         for (int64_t k = 0; k < n; k += per_tile)
             g->tiles.push_back({(int32_t)i, (int32_t)std::min(per_tile, n - k), k});
     }
@@ -169,7 +188,7 @@ NormArgs norm_args(shampoo_gradnorm_s* h) {
     a.ntiles = (int32_t)h->tiles.size();
     a.pieces = h->pieces;
     a.partials = reinterpret_cast<double*>(h->arena + h->off_partials);
-    a.ticket = reinterpret_cast<int32_t*>(h->arena + h->off_ticket);
+    a.tickets = reinterpret_cast<int32_t*>(h->arena + h->off_tickets);
     a.record = reinterpret_cast<ClipRecord*>(h->arena + h->off_record);
     return a;
 }
@@ -263,6 +282,16 @@ int shampoo_adamw_bind_tensors(shampoo_adamw_t* h, void* const* params, const vo
         if (params && (!params[i] || !aligned_to(params[i], dtype_bytes(d.param_type))))
             return SHAMPOO_E_ARG;
         if (grads && !aligned_to(grads[i], dtype_bytes(d.grad_type))) return SHAMPOO_E_ARG;
+    }
+    if (params) {   // a weight that is listed twice would be updated by two waves at once
+        try {
+            std::vector<Span> spans;
+            for (int i = 0; i < n; ++i)
+                add_span(spans, params[i], h->desc[i].numel * (int64_t)dtype_bytes(h->desc[i].param_type));
+            if (overlap(spans)) return SHAMPOO_E_ARG;
+        } catch (const std::bad_alloc&) {
+            return SHAMPOO_E_NOMEM;
+        }
     }
     AdamwTensor* table = reinterpret_cast<AdamwTensor*>(h->arena + h->off_table);
     for (int i = 0; i < n; i += kBindBatch) {
@@ -367,7 +396,7 @@ int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
         return o;
     };
     h->off_record = take(sizeof(ClipRecord));
-    h->off_ticket = take(4);
+    h->off_tickets = take(128 * (kNormGroups + 1));
     h->off_partials = take(8 * (int64_t)norm_grid((int64_t)h->tiles.size()));
     h->off_table = take((int64_t)(h->table.size() * sizeof(NormTensor)));
     h->off_tiles = take((int64_t)(h->tiles.size() * sizeof(NormTile)));
@@ -415,8 +444,31 @@ int shampoo_gradnorm_bind_grads(shampoo_gradnorm_t* h, const void* const* grads,
         if (t.numel == 0) continue;
         if (!aligned_to(grads[i], dtype_bytes(t.dtype))) return SHAMPOO_E_ARG;
         if (outs && !aligned_to(outs[i], 4)) return SHAMPOO_E_ARG;
-        // in place only where an element's output lies where its input did
-        if (outs && outs[i] && outs[i] == grads[i] && t.dtype != SHAMPOO_F32) return SHAMPOO_E_ARG;
+    }
+    if (outs) {
+        // outputs overlap neither each other nor a gradient, but for an fp32
+        // gradient that is its own output
+        try {
+            std::vector<Span> spans;
+            for (int i = 0; i < n; ++i) {
+                const NormTensor& t = h->table[i];
+                add_span(spans, outs[i], 4 * t.numel);
+            }
+            if (overlap(spans)) return SHAMPOO_E_ARG;
+            for (int i = 0; i < n; ++i) {
+                const NormTensor& t = h->table[i];
+                if (outs[i] && (const void*)outs[i] == grads[i] && t.dtype == SHAMPOO_F32) continue;
+                const uint64_t b = reinterpret_cast<uint64_t>(grads[i]);
+                const uint64_t e = b + (uint64_t)t.numel * dtype_bytes(t.dtype);
+                if (!b || t.numel == 0) continue;
+                // the spans are sorted and apart: the first that ends after b
+                const auto it = std::upper_bound(spans.begin(), spans.end(), b,
+                                                 [](uint64_t x, const Span& s) { return x < s.end; });
+                if (it != spans.end() && it->begin < e) return SHAMPOO_E_ARG;
+            }
+        } catch (const std::bad_alloc&) {
+            return SHAMPOO_E_NOMEM;
+        }
     }
     NormTensor* table = reinterpret_cast<NormTensor*>(h->arena + h->off_table);
     for (int i = 0; i < n; i += kBindBatch) {
@@ -438,9 +490,8 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
         return SHAMPOO_E_ARG;
     if (!h->bound || !h->grads_bound || !on_device(h->device)) return SHAMPOO_E_STATE;
     NormArgs a = norm_args(h);
-    // gradients that fit the last-level cache are found there by the step that
-    // follows (302M bf16 elements: 93 us past the caches, 103 through them)
-    a.stream_past = h->grad_bytes > kCacheBytes;
+    // (302M bf16 elements: 93 us past the caches, 103 through them)
+    a.stream_past = h->grad_bytes > kGradCacheBytes;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
     return status_of(launch_norm(a, static_cast<hipStream_t>(stream)));

@@ -495,18 +495,35 @@ __global__ __launch_bounds__(256) void k_norm_bind(NormTensor* tensors, int n, P
 }
 
 // ------------------------------------------------------------ gradient norm
-__device__ __forceinline__ double wave_sum_d(double v) {
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+// Sum over the 64 lanes of a wave by lane permutations inside the ALU: pairs,
+// quads, rows of 16, then rows 0 and 2 into 1 and 3, and row 1 into row 3,
+// whose last lane is read out.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved_d(double v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROWS, 0xf, false);
+    return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double wave_total(double v) {
+    v += moved_d<0xB1, 0xf>(v);    // quad_perm [1,0,3,2]
+    v += moved_d<0x4E, 0xf>(v);    // quad_perm [2,3,0,1]
+    v += moved_d<0x141, 0xf>(v);   // the other quad of eight
+    v += moved_d<0x140, 0xf>(v);   // the other eight of a row
+    v += moved_d<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
+    v += moved_d<0x143, 0xc>(v);   // row_bcast:31 into rows 2 and 3
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                            __builtin_amdgcn_readlane(__double2loint(v), 63));
 }
 // The sum over a workgroup of kNormWaves waves, to every lane.
 __device__ __forceinline__ double group_sum(double v, double* red) {
-    v = wave_sum_d(v);
+    v = wave_total(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    const int l = threadIdx.x & 63;
-    return wave_sum_d(l < kNormWaves ? red[l] : 0.0);
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kNormWaves; ++w) t += red[w];
+    return t;
 }
 
 // 16 bytes of a gradient per lane and load: a wave reads a piece of kNormPiece
@@ -618,8 +635,19 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_norm(NormArgs a) {
         // after another.
         __hip_atomic_store(a.partials + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               (int)gridDim.x - 1;
+        // counts of one address are 12 ns one after another: a large grid
+        // counts in groups, and the last of each group among the groups
+        const int n = (int)gridDim.x, groups = n > 2 * kNormGroups ? kNormGroups : 1;
+        const int g = (int)blockIdx.x % groups;
+        int32_t* ticket = a.tickets + 32 * g;
+        last = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (n - g + groups - 1) / groups - 1;
+        if (last) {
+            *ticket = 0;   // for the next launch
+            if (groups > 1)
+                last = __hip_atomic_fetch_add(a.tickets + 32 * kNormGroups, 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
+        }
     }
     __syncthreads();
     if (!last) return;
@@ -637,7 +665,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_norm(NormArgs a) {
         r.nonfinite = finite ? 0 : 1;
         r.pad_ = 0;
         *a.record = r;
-        *a.ticket = 0;   // for the next launch
+        a.tickets[32 * kNormGroups] = 0;
     }
 }
 
@@ -708,8 +736,7 @@ hipError_t go_grad(int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {
 // Four tiles, one per wave, to a workgroup.
 int adamw_grid(int64_t ntiles) { return (int)((ntiles + 3) / 4); }
 // At most two workgroups of eight waves on each of the 256 CUs (302M bf16
-// elements: 103 us; with 16 waves 108, with 1024 workgroups of four 105): they
-// are counted one after another, 12 ns each.
+// elements: 103 us; with 16 waves 108, with 1024 workgroups of four 105).
 int norm_grid(int64_t ntiles) {
     return (int)(ntiles < 512 * kNormWaves ? (ntiles + kNormWaves - 1) / kNormWaves + (ntiles == 0) : 512);
 }

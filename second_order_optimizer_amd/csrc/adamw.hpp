@@ -82,6 +82,7 @@ struct NormTile {
     int64_t first;            // first element of the tile
 };
 constexpr int kNormWaves = 8;    // waves of a workgroup of the norm
+constexpr int kNormGroups = 16;   // groups that a large grid counts its workgroups in
 constexpr int kNormPiece = 1024;  // elements that a wave has in flight together; a tile is some
 
 struct NormArgs {
@@ -89,7 +90,7 @@ struct NormArgs {
     const NormTile* tiles;
     int32_t ntiles, pieces;   // pieces of a tile
     double* partials;         // one per workgroup
-    int32_t* ticket;
+    int32_t* tickets;         // kNormGroups + 1 counts, 128 bytes apart
     int32_t stream_past, pad_; // the gradients are more than the caches hold
     ClipRecord* record;
     double max_norm, grad_scale;

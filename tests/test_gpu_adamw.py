@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+FILLER = 1 << 20        # tensors larger than this only fill a plan and are not checked
 GUARD = 16      # elements beside a tensor that nothing may touch
 SENTINEL = -77.0
 
@@ -51,7 +52,8 @@ class Run:
         self.sigma = [10 ** self.rng.uniform(-4, 0) for _ in specs]
         self.params, self.grads, self.bufs = [], [], []
         for s, dt in zip(specs, self.types):
-            w = (0.02 * self.rng.standard_normal(s.numel)).astype(np.float32)
+            w = (0.02 * self.rng.standard_normal(min(s.numel, FILLER))).astype(np.float32)
+            w = np.resize(w, s.numel)
             t, b = guarded(w, TORCH[dt], offset)
             self.params.append(t)
             self.bufs.append((b, s.numel))
@@ -66,6 +68,8 @@ class Run:
         self.opt.bind(self.params, self.grads)
 
     def draw(self, i):
+        if self.specs[i].numel > FILLER:
+            return np.zeros(self.specs[i].numel, np.float32)
         return (self.sigma[i] * self.rng.standard_normal(self.specs[i].numel)).astype(np.float32)
 
     def place(self, i):
@@ -95,6 +99,8 @@ class Run:
         for i, s in enumerate(self.specs):
             q = self.parts(i)
             n, runs = s.numel, -(-s.numel // 256)
+            if n > FILLER:
+                continue
             if "m" in q:
                 q["m"].copy_(torch.from_numpy(0.3 * self.draw(i)))
                 q["v"].copy_(torch.from_numpy(self.draw(i) ** 2))
@@ -119,6 +125,9 @@ class Run:
         for i, s in enumerate(self.specs):
             q = {k: x.cpu().numpy().copy() for k, x in self.parts(i).items()}
             w = self.params[i].detach().cpu()
+            if s.numel > FILLER:
+                got.append(q)
+                continue
             if "rem" in q:
                 q["p"] = O.bf16_join(w.view(torch.int16).numpy().view(np.uint16), q["rem"]).astype(np.float64)
             else:
@@ -150,7 +159,7 @@ class Run:
         after = self.read()
         for i, (a, b) in enumerate(zip(before, after)):
             s = self.specs[i]
-            if s.numel == 0:
+            if s.numel == 0 or s.numel > FILLER:
                 continue
             # eps and the scalars reach the kernel as fp32: within U of these
             p, m, root, v, pe, me, re, ve = O.step(a["p"], a["g"], a["m"], a["v"], self.t,
@@ -209,6 +218,43 @@ def test_step(param, grad, bits, offset):
         for i, g in enumerate(run.grads):
             g.copy_(torch.from_numpy(run.draw(i)))
     run.rest_untouched()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,grad", [("f32", "f32"), ("f32", "bf16"), ("f32", "f16"),
+                                        ("bf16", "bf16"), ("bf16", "f32"), ("bf16", "f16")])
+def test_step_past_the_caches(param, grad, bits):
+    """A plan of more than 96 MiB takes the kernels that pass the caches by."""
+    specs = [A.tensor(n, param=param, grad=grad, state_bits=bits, weight_decay=0.1) for n in SIZES]
+    run = Run(specs[:8] + [A.tensor(13 << 20, param=param, grad=grad, state_bits=bits)] + specs[8:], 31, offset=1)
+    for lr in (1e-3, 3e-4):
+        before = run.read()
+        run.opt.step(lr)
+        run.check(before, lr)
+        for i, g in enumerate(run.grads):
+            g.copy_(torch.from_numpy(run.draw(i)))
+    run.rest_untouched()
+
+
+def test_saved_and_restored():
+    """Steps after a restored state are the steps that would have followed."""
+    specs = [A.tensor(n, param=p, state_bits=b, grad="bf16") for n in (700, 5000) for p in ("f32", "bf16") for b in (32, 8)]
+    a, b = Run(specs, 4), Run(specs, 4, warm=False)
+    for _ in range(3):
+        a.opt.step(1e-3)
+    saved = a.opt.state_dict()
+    for x, y in zip(b.params, a.params):
+        x.copy_(y)
+    b.opt.load_state_dict(saved)
+    for r in (a, b):
+        for _ in range(2):
+            r.opt.step(1e-3)
+    assert int(b.opt.t) == 5
+    for x, y in zip(a.read(), b.read()):
+        for k in x:
+            assert np.array_equal(x[k], y[k], equal_nan=True), k
+    with pytest.raises(ValueError):
+        A.AdamW(specs[:3]).load_state_dict(saved)
 
 
 def test_first_steps_from_nothing():
@@ -586,6 +632,23 @@ def test_norm(offset, scale, grad_scale):
     assert torch.equal(first, norm.record)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_norm_past_the_caches(kind):
+    """More than 192 MiB of gradients; one value in each of a few places."""
+    n = (204 << 20) // (4 if kind == "f32" else 2) + 77
+    g = torch.zeros(n + 3, dtype=TORCH[kind], device="cuda")[3:]
+    for i, k in enumerate((0, 1023, 1024, n // 2, n - 78, n - 1)):
+        g[k] = 2.0 ** i
+    small = torch.full((5,), 0.5, dtype=TORCH[kind], device="cuda")
+    norm = A.GradNorm([(5, kind), (n, kind)])
+    norm.bind([small, g])
+    for _ in range(3):
+        norm.compute(1.0)
+        want = np.sqrt(5 * 0.25 + sum(4.0 ** i for i in range(6)))
+        assert abs(float(norm.record[0]) - want) <= 2 * O.U * want
+        assert abs(float(norm.record[1]) - 1 / want) <= 2 * O.U / want
+
+
 def test_norm_clips_in_place_and_leaves_absent_ones():
     rng = np.random.default_rng(3)
     a, b, c = (torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda() for n in (5000, 300, 40))
@@ -645,6 +708,12 @@ def test_refusals():
             opt.bind(bad)
     with pytest.raises(S.ShampooError):
         opt.bind()
+    twice = A.AdamW([A.tensor(8), A.tensor(4), A.tensor(0)])
+    nothing = torch.empty(0, device="cuda")
+    for bad in ([p[0], p[0][:4], nothing], [p[0], p[0][4:], nothing]):
+        with pytest.raises(S.ShampooError):
+            twice.bind(bad)                               # a weight that is listed twice
+    twice.bind([p[0], torch.zeros(4, device="cuda"), nothing])
     with pytest.raises(ValueError):
         opt.step(torch.tensor([1e-3]))
     with pytest.raises(ValueError):
@@ -663,6 +732,14 @@ def test_refusals():
     norm.bind([p[1]])
     with pytest.raises(S.ShampooError):
         norm.compute(0.0)
+    two = A.GradNorm([(4, "f32"), (4, "f32")])
+    x = torch.zeros(16, device="cuda")
+    two.bind([x[:4], x[4:8]], [x[:4], x[8:12]])
+    for outs in ([x[4:8], None], [x[2:6], None], [x[8:12], x[10:14]], [x[:4], x[3:7]]):
+        with pytest.raises(S.ShampooError):
+            two.bind([x[:4], x[4:8]], outs)
+    with pytest.raises(ValueError):
+        A.AdamW([A.tensor(4)], device="cpu")
 
 
 # ------------------------------------------------------------ as they are used
