@@ -1,8 +1,8 @@
 // C-ABI of the first-order operators: the plan and launch sequence of one
 // AdamW step over many tensors, and of the global gradient norm.
 //
-// A plan cuts every tensor into runs of 256 elements and hands a few runs at
-// a time to a wave, so that hundreds of small tensors and a few huge ones are
+// A plan cuts every tensor into runs of 256 elements and hands a few runs to
+// each workgroup, so that hundreds of small tensors and a few huge ones are
 // one launch.  Nothing is uploaded by a step: the tables lie in the caller's
 // state buffer, tensor addresses reach it as kernel arguments when they are
 // bound, and the step counter lives on the device, so a step can be captured
@@ -109,14 +109,7 @@ AdamwClock clock_at(const shampoo_adamw_config& c, int64_t t) {
 }
 
 void plan_adamw(shampoo_adamw_s* h) {
-    int64_t runs[2] = {0, 0}, rem_runs = 0, total_runs = 0;
-    for (const auto& d : h->desc) total_runs += runs_of(d.numel);
-    // A wave takes two runs at a time, one to each half, and one such pair is a
-    // tile.  With 8-bit moments, where a pair is half the bytes, tiles of two
-    // pairs once there are four waves for each SIMD (302M bf16 elements: 700
-    // us, 721 with one pair; 1M: 6.3 and 5.5 us.  fp32 moments, 302M fp32
-    // elements: 1428 us with one pair, 1487 with two).
-    const int64_t wide = total_runs >= 4 * 4096 ? 4 : 2;
+    int64_t runs[2] = {0, 0}, rem_runs = 0;
     for (size_t i = 0; i < h->desc.size(); ++i) {
         const auto& d = h->desc[i];
         AdamwTensor t{};
@@ -143,9 +136,7 @@ void plan_adamw(shampoo_adamw_s* h) {
             g->grad = d.grad_type;
             g->bits8 = d.state_bits == 8;
         }
-        const int64_t per_tile = d.state_bits == 8 ? wide : 2;
-        for (int64_t k = 0; k < n; k += per_tile)
-            g->tiles.push_back({(int32_t)i, (int32_t)std::min(per_tile, n - k), k});
+        for (int64_t k = 0; k < n; k += kTileRuns) g->tiles.push_back({(int32_t)i, 0, k});
     }
     int64_t at = 0;
     const auto take = [&at](int64_t bytes) {
@@ -155,7 +146,7 @@ void plan_adamw(shampoo_adamw_s* h) {
     };
     for (auto& g : h->groups) {
         g.off_clocks = (int64_t)h->nclocks * (int64_t)sizeof(AdamwClock);
-        h->nclocks += adamw_grid((int64_t)g.tiles.size());
+        h->nclocks += (int)g.tiles.size();
     }
     h->nclocks = std::max(h->nclocks, 1);
     h->lay.off_clock = take((int64_t)h->nclocks * (int64_t)sizeof(AdamwClock));
@@ -214,7 +205,7 @@ int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,
             d.grad_type > SHAMPOO_F16 || (d.state_bits != 8 && d.state_bits != 32))
             return SHAMPOO_E_ARG;
         if (d.param_type == SHAMPOO_F16 || d.numel > kMaxNumel) return SHAMPOO_E_UNSUPPORTED;
-        tiles += runs_of(d.numel) / 2 + 1;
+        tiles += runs_of(d.numel) / kTileRuns + 1;
         if (tiles > kMaxTiles) return SHAMPOO_E_UNSUPPORTED;
     }
     shampoo_adamw_s* h = new (std::nothrow) shampoo_adamw_s();

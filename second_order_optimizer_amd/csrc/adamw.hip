@@ -25,9 +25,10 @@ namespace {
 // anywhere (gfx950 loads and stores 16 bytes at any address).
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned short u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
@@ -51,6 +52,24 @@ __device__ __forceinline__ void st(T* p, T x) {
     if constexpr (NT) __builtin_nontemporal_store(x, p);
     else *p = x;
 }
+
+// The same at any address that suits an element (a template argument would
+// lose the vector's alignment, so each type has its own).
+#define SHAMPOO_LOOSE(V)                                                  \
+    template <bool NT>                                                    \
+    __device__ __forceinline__ V ld_loose(const V* p) {                   \
+        if constexpr (NT) return __builtin_nontemporal_load(p);           \
+        else return *p;                                                   \
+    }                                                                     \
+    template <bool NT>                                                    \
+    __device__ __forceinline__ void st_loose(V* p, V x) {                 \
+        if constexpr (NT) __builtin_nontemporal_store(x, p);              \
+        else *p = x;                                                      \
+    }
+SHAMPOO_LOOSE(f32x4u)
+SHAMPOO_LOOSE(u32x2h)
+SHAMPOO_LOOSE(u32x4h)
+#undef SHAMPOO_LOOSE
 
 template <int DT> struct Elem { typedef unsigned short type; };
 template <> struct Elem<DT_F32> { typedef float type; };
@@ -83,25 +102,36 @@ __device__ __forceinline__ f32x4 widen4(const Raw<DT>& r) {
     }
 }
 
-// Four consecutive elements from `first` of a tensor; FULL: all four exist,
-// else those past `numel` read as 0.
+// A lane's address: a base that the whole wave shares (in scalar registers),
+// the lane's own 32-bit byte offset, and a constant.
+template <typename T>
+__device__ __forceinline__ T* lane_at(uint64_t base, uint32_t bytes, int add) {
+    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type C;
+    return reinterpret_cast<T*>(gptr<C>(base) + bytes + add);
+}
+
+// Four consecutive elements, from element lane + add of what starts at `base`
+// and has `rest` elements; FULL: all four exist, else those past the end read
+// as 0.
 template <int DT, bool FULL, bool NT = false>
-__device__ __forceinline__ Raw<DT> load4(uint64_t base, int64_t first, int64_t numel) {
+__device__ __forceinline__ Raw<DT> load4(uint64_t base, uint32_t lane, int add, int64_t rest) {
     typedef typename Elem<DT>::type T;
-    const uint64_t at = base + (uint64_t)first * sizeof(T);
+    constexpr int kSize = (int)sizeof(T);
+    const T* p = lane_at<const T>(base, lane * kSize, add * kSize);
+    const int64_t left = rest - ((int64_t)lane + add);
     Raw<DT> r;
     if constexpr (DT == DT_F32) {
-        if (FULL || first + 4 <= numel) {
-            r.w = ld<NT>(gptr<const f32x4u>(at));
+        if (FULL || left >= 4) {
+            r.w = ld_loose<NT>(reinterpret_cast<const f32x4u*>(p));
         } else {
-            for (int k = 0; k < 4; ++k) r.w[k] = first + k < numel ? gptr<const T>(at)[k] : 0.f;
+            for (int k = 0; k < 4; ++k) r.w[k] = k < left ? p[k] : 0.f;
         }
     } else {
-        if (FULL || first + 4 <= numel) {
-            r.w = ld<NT>(gptr<const u32x2h>(at));
+        if (FULL || left >= 4) {
+            r.w = ld_loose<NT>(reinterpret_cast<const u32x2h*>(p));
         } else {
             uint32_t u[4];
-            for (int k = 0; k < 4; ++k) u[k] = first + k < numel ? gptr<const T>(at)[k] : 0u;
+            for (int k = 0; k < 4; ++k) u[k] = k < left ? p[k] : 0u;
             r.w = u32x2{u[0] | u[1] << 16, u[2] | u[3] << 16};
         }
     }
@@ -109,22 +139,24 @@ __device__ __forceinline__ Raw<DT> load4(uint64_t base, int64_t first, int64_t n
 }
 
 template <int DT, bool FULL, bool NT = false>
-__device__ __forceinline__ void store4(uint64_t base, int64_t first, int64_t numel, const Raw<DT>& r) {
+__device__ __forceinline__ void store4(uint64_t base, uint32_t lane, int add, int64_t rest, const Raw<DT>& r) {
     typedef typename Elem<DT>::type T;
-    const uint64_t at = base + (uint64_t)first * sizeof(T);
+    constexpr int kSize = (int)sizeof(T);
+    T* p = lane_at<T>(base, lane * kSize, add * kSize);
+    const int64_t left = rest - ((int64_t)lane + add);
     if constexpr (DT == DT_F32) {
-        if (FULL || first + 4 <= numel) {
-            st<NT>(gptr<f32x4u>(at), (f32x4u)r.w);
+        if (FULL || left >= 4) {
+            st_loose<NT>(reinterpret_cast<f32x4u*>(p), r.w);
         } else {
             for (int k = 0; k < 4; ++k)
-                if (first + k < numel) gptr<T>(at)[k] = r.w[k];
+                if (k < left) p[k] = r.w[k];
         }
     } else {
-        if (FULL || first + 4 <= numel) {
-            st<NT>(gptr<u32x2h>(at), (u32x2h)r.w);
+        if (FULL || left >= 4) {
+            st_loose<NT>(reinterpret_cast<u32x2h*>(p), r.w);
         } else {
             for (int k = 0; k < 4; ++k)
-                if (first + k < numel) gptr<T>(at)[k] = (T)(r.w[k >> 1] >> (16 * (k & 1)));
+                if (k < left) p[k] = (T)(r.w[k >> 1] >> (16 * (k & 1)));
         }
     }
 }
@@ -227,8 +259,7 @@ __device__ __forceinline__ f32x4 decode4(uint32_t w) {
 // offset, in bits that the shift does not reach.  ANY: the run holds values
 // below 2^-6 of e4m3's range or not finite.
 template <bool ANY, bool NT>
-__device__ __forceinline__ void encode_run(const AdamwArgs& a, const f32x4* m, const f32x4* root, float mi,
-                                           float si, uint32_t start, int64_t at) {
+__device__ __forceinline__ void encode_run(const f32x4* m, const f32x4* root, float mi, float si, uint32_t start, uint64_t m8, uint64_t s8, uint32_t lo) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint32_t h[4], mw = 0, sw = 0;
@@ -259,21 +290,30 @@ __device__ __forceinline__ void encode_run(const AdamwArgs& a, const f32x4* m, c
             sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][2] * si, h[2] & 0xFFFF0000u, (int)sw, 2);
             sw = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(root[j][3] * si, h[3] & 0xFFFF0000u, (int)sw, 3);
         }
-        st<NT>(reinterpret_cast<uint32_t*>(a.m8 + at + 128 * j), mw);
-        st<NT>(reinterpret_cast<uint32_t*>(a.s8 + at + 128 * j), sw);
+        st<NT>(lane_at<uint32_t>(m8, lo, 128 * j), mw);
+        st<NT>(lane_at<uint32_t>(s8, lo, 128 * j), sw);
     }
 }
 
-// One run of 256 elements by half a wave: lane l (of 32) takes the elements
-// 4l.. and 128 + 4l.., so that every load and store of the half covers whole
-// 128-byte lines.
+// Two runs of 256 elements from `run`, one to each half of the wave: lane l
+// (of 32) takes the elements 4l.. and 128 + 4l.. of its run, so that every
+// load and store of a half covers whole 128-byte lines.  Without FULL the runs
+// are those that the tensor ends in, and the second half may be idle.
 template <int P, int G, bool S8, bool FULL, bool NT>
-__device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& ts, int64_t run, int l,
-                                         float coef, float fa, float fb, float root_c, uint32_t key) {
+__device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor& ts, int64_t run, float coef,
+                                          float fa, float fb, float root_c, uint32_t key) {
+    const int l = threadIdx.x & 31;
+    const uint32_t half = (threadIdx.x >> 5) & 1;
+    const uint32_t lo = half * kRun + 4 * l;                  // the lane's first element
     const int64_t sr = ts.state_run + run;
-    const int64_t at = sr * kRun + 4 * l;
-    const int64_t e0 = run * kRun + 4 * l;
-    const int64_t rm = (ts.rem_run + run) * kRun + 4 * l;
+    const int64_t rest = ts.numel - run * kRun;               // elements from the first run on
+    const uint64_t gb = ts.g_ptr + (uint64_t)run * kRun * sizeof(typename Elem<G>::type);
+    const uint64_t pb = ts.p_ptr + (uint64_t)run * kRun * sizeof(typename Elem<P>::type);
+    const uint64_t rb = reinterpret_cast<uint64_t>(a.rem + (ts.rem_run + run) * kRun);
+    const uint64_t mb = S8 ? reinterpret_cast<uint64_t>(a.m8 + sr * kRun) : reinterpret_cast<uint64_t>(a.m + sr * kRun);
+    const uint64_t vb = S8 ? reinterpret_cast<uint64_t>(a.s8 + sr * kRun) : reinterpret_cast<uint64_t>(a.v + sr * kRun);
+    const uint64_t msb = reinterpret_cast<uint64_t>(a.m_scale + sr);
+    const uint64_t ssb = reinterpret_cast<uint64_t>(a.s_scale + sr);
     Raw<G> graw[2];
     Raw<P> praw[2];
     u32x2 rem[2];
@@ -281,20 +321,20 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
     f32x4 m[2], v[2];
     float ms = 0.f, ss = 0.f;
     if constexpr (S8) {
-        ms = a.m_scale[sr];
-        ss = a.s_scale[sr];
+        ms = *lane_at<const float>(msb, 4 * half, 0);
+        ss = *lane_at<const float>(ssb, 4 * half, 0);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        graw[j] = load4<G, FULL, NT>(ts.g_ptr, e0 + 128 * j, ts.numel);
-        praw[j] = load4<P, FULL, NT>(ts.p_ptr, e0 + 128 * j, ts.numel);
-        if constexpr (P == DT_BF16) rem[j] = ld<NT>(reinterpret_cast<const u32x2*>(a.rem + rm + 128 * j));
+        graw[j] = load4<G, FULL, NT>(gb, lo, 128 * j, rest);
+        praw[j] = load4<P, FULL, NT>(pb, lo, 128 * j, rest);
+        if constexpr (P == DT_BF16) rem[j] = ld<NT>(lane_at<const u32x2>(rb, 2 * lo, 256 * j));
         if constexpr (S8) {
-            mw[j] = ld<NT>(reinterpret_cast<const uint32_t*>(a.m8 + at + 128 * j));
-            sw[j] = ld<NT>(reinterpret_cast<const uint32_t*>(a.s8 + at + 128 * j));
+            mw[j] = ld<NT>(lane_at<const uint32_t>(mb, lo, 128 * j));
+            sw[j] = ld<NT>(lane_at<const uint32_t>(vb, lo, 128 * j));
         } else {
-            m[j] = ld<NT>(reinterpret_cast<const f32x4*>(a.m + at + 128 * j));
-            v[j] = ld<NT>(reinterpret_cast<const f32x4*>(a.v + at + 128 * j));
+            m[j] = ld<NT>(lane_at<const f32x4>(mb, 4 * lo, 512 * j));
+            v[j] = ld<NT>(lane_at<const f32x4>(vb, 4 * lo, 512 * j));
         }
     }
     uint32_t vmin = 0xFFFFFFFFu;
@@ -366,20 +406,21 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
             // 2^15, and what is left, as a signed number, is the lower half of
             // bits; a NaN becomes the quiet NaN without remainder
             uint32_t b[4];
-            for (int q = 0; q < 4; ++q)
-                b[q] = w[q] != w[q] ? 0x7FC00000u : __float_as_uint(w[q]);
+            for (int q = 0; q < 4; ++q) b[q] = __float_as_uint(w[q]);
+            if (__any(__builtin_isunordered(w[0], w[1]) || __builtin_isunordered(w[2], w[3])))
+                for (int q = 0; q < 4; ++q) b[q] = w[q] != w[q] ? 0x7FC00000u : b[q];
             for (int k = 0; k < 2; ++k) {
                 out.w[k] = __builtin_amdgcn_perm(b[2 * k + 1] + 0x8000u, b[2 * k] + 0x8000u, 0x07060302u);
                 left[k] = __builtin_amdgcn_perm(b[2 * k + 1], b[2 * k], 0x05040100u);
             }
-            st<NT>(reinterpret_cast<u32x2*>(a.rem + rm + 128 * j), left);
+            st<NT>(lane_at<u32x2>(rb, 2 * lo, 256 * j), left);
         } else {
             out.w = w;
         }
-        store4<P, FULL, NT>(ts.p_ptr, e0 + 128 * j, ts.numel, out);
+        store4<P, FULL, NT>(pb, lo, 128 * j, rest, out);
         if constexpr (!S8) {
-            st<NT>(reinterpret_cast<f32x4*>(a.m + at + 128 * j), m[j]);
-            st<NT>(reinterpret_cast<f32x4*>(a.v + at + 128 * j), v[j]);
+            st<NT>(lane_at<f32x4>(mb, 4 * lo, 512 * j), m[j]);
+            st<NT>(lane_at<f32x4>(vb, 4 * lo, 512 * j), v[j]);
         }
     }
     if constexpr (S8) {
@@ -416,19 +457,29 @@ __device__ __forceinline__ void step_run(const AdamwArgs& a, const AdamwTensor& 
         float scale, inv, mi, si;
         run_scale(top, scale, inv);
         half_both(inv, mi, si);
-        if ((l & 15) == 0) (l == 0 ? a.m_scale : a.s_scale)[sr] = scale;
-        uint32_t start = (key + (uint32_t)((uint64_t)e0 >> 32) * 0x85157AF5u) ^ (uint32_t)e0;
+        if (l == 0) *lane_at<float>(msb, 4 * half, 0) = scale;
+        if (l == 16) *lane_at<float>(ssb, 4 * half, 0) = scale;
+        // the element's index: two runs from an even one share its upper half
+        const uint64_t e0 = (uint64_t)run * kRun;
+        uint32_t start = (key + (uint32_t)(e0 >> 32) * 0x85157AF5u) ^ ((uint32_t)e0 | lo);
         start ^= start >> 16;
         if (__any(mlow * mi < 0x1p-6f || slow * si < 0x1p-6f) || odd)
-            encode_run<true, NT>(a, m, root, mi, si, start, at);
+            encode_run<true, NT>(m, root, mi, si, start, mb, vb, lo);
         else
-            encode_run<false, NT>(a, m, root, mi, si, start, at);
+            encode_run<false, NT>(m, root, mi, si, start, mb, vb, lo);
     }
 }
 
-// One step of the elements of this wave's tiles.
+// One step of the elements of this workgroup's tile.
+//
+// Waves per SIMD are held below what the registers would allow: more of them
+// spread the accesses over more of the memory's pages at once.  fp32 moments,
+// 302M fp32 elements: 1367 us with 4, 1385 with 6, 1434 (up to 1520) with 8.
+// 8-bit moments need more for the arithmetic, 302M / 60M bf16 elements: 805 /
+// 192 us with 3, 730 / 177 with 4, 690 / 165 with 6, 715 (up to 752) / 164
+// with 7.
 template <int P, int G, bool S8, bool NT>
-__global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, S8 ? 6 : 4))) void k_adamw(AdamwArgs a) {
     // field by field: a copy of the whole struct, its padding included, went
     // through LDS and cost 14 us at 256 workgroups
     AdamwClock* clock = a.clocks + blockIdx.x;
@@ -441,25 +492,19 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         coef = a.clip->coef;
     }
     const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
-    const int lane = threadIdx.x & 63, l = lane & 31;
-    const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     const uint32_t key0 = mix32(a.seed_mixed + (uint32_t)(t + 1));
-    if (wave < a.ntiles) {
-        const AdamwTile tl = a.tiles[wave];
-        const AdamwTensor ts = a.tensors[tl.tensor];
-        const float fa = (float)(lr * ts.lr_scale * ts.weight_decay);
-        const float fb = (float)(lr * ts.lr_scale * inv1);
-        const uint32_t key = mix32(key0 + (uint32_t)ts.id);
-        // two runs at a time, one to each half; an odd last run is taken by
-        // both halves' lanes together with a run that has no elements
-        const int nruns = ts.g_ptr ? tl.nruns : 0;
-        for (int k = 0; k < nruns; k += 2) {
-            const int64_t run = tl.run0 + k + (lane >> 5);
-            if ((tl.run0 + k + 2) * kRun <= ts.numel)
-                step_run<P, G, S8, true, NT>(a, ts, run, l, coef, fa, fb, root_c, key);
-            else if (run * kRun < ts.numel)
-                step_run<P, G, S8, false, false>(a, ts, run, l, coef, fa, fb, root_c, key);
-        }
+    const AdamwTile tl = a.tiles[blockIdx.x];
+    const AdamwTensor ts = a.tensors[tl.tensor];
+    const float fa = (float)(lr * ts.lr_scale * ts.weight_decay);
+    const float fb = (float)(lr * ts.lr_scale * inv1);
+    const uint32_t key = mix32(key0 + (uint32_t)ts.id);
+    // two runs to each of the four waves
+    const int64_t run = tl.run0 + 2 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (ts.g_ptr) {
+        if ((run + 2) * kRun <= ts.numel)
+            step_runs<P, G, S8, true, NT>(a, ts, run, coef, fa, fb, root_c, key);
+        else if ((run + ((threadIdx.x >> 5) & 1)) * kRun < ts.numel)
+            step_runs<P, G, S8, false, false>(a, ts, run, coef, fa, fb, root_c, key);
     }
     __syncthreads();   // every wave has read the clock
     if (threadIdx.x == 0) {
@@ -528,8 +573,6 @@ __device__ __forceinline__ double group_sum(double v, double* red) {
 
 // 16 bytes of a gradient per lane and load: a wave reads a piece of kNormPiece
 // elements with all its loads in flight.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
 template <int DT> struct Piece {
     static constexpr int kPer = DT == DT_F32 ? 4 : 8;          // elements of a load
     static constexpr int kLoads = kNormPiece / 64 / kPer;
@@ -543,7 +586,7 @@ __device__ __forceinline__ void load_piece(Piece<DT>& r, uint64_t g, int64_t fir
     if (first + kNormPiece <= numel) {
 #pragma unroll
         for (int k = 0; k < Piece<DT>::kLoads; ++k)
-            r.w[k] = ld<NT>(gptr<const u32x4h>(g + (uint64_t)(first + (k * 64 + lane) * kPer) * sizeof(T)));
+            r.w[k] = ld_loose<NT>(gptr<const u32x4h>(g + (uint64_t)(first + (k * 64 + lane) * kPer) * sizeof(T)));
         return;
     }
     for (int k = 0; k < Piece<DT>::kLoads; ++k) {
@@ -671,16 +714,19 @@ __global__ __launch_bounds__(64 * kNormWaves) void k_norm(NormArgs a) {
 
 template <int DT, bool FULL>
 __device__ __forceinline__ void piece_clip(const NormTensor& ts, int64_t first, int lane, float coef, bool zero) {
+    const int64_t rest = ts.numel - first;
+    const uint64_t gb = ts.g_ptr + (uint64_t)first * sizeof(typename Elem<DT>::type);
+    const uint64_t ob = ts.out_ptr + (uint64_t)first * 4;
     Raw<DT> raw[kNormPiece / 256];
 #pragma unroll
     for (int k = 0; k < kNormPiece / 256; ++k)
-        raw[k] = load4<DT, FULL>(ts.g_ptr, first + k * 256 + lane * 4, ts.numel);
+        raw[k] = load4<DT, FULL>(gb, 4 * lane, 256 * k, rest);
 #pragma unroll
     for (int k = 0; k < kNormPiece / 256; ++k) {
         const f32x4 x = widen4<DT>(raw[k]);
         Raw<DT_F32> y;
         for (int q = 0; q < 4; ++q) y.w[q] = zero ? 0.f : x[q] * coef;
-        store4<DT_F32, FULL>(ts.out_ptr, first + k * 256 + lane * 4, ts.numel, y);
+        store4<DT_F32, FULL>(ob, 4 * lane, 256 * k, rest, y);
     }
 }
 template <int DT>
@@ -713,7 +759,7 @@ __global__ __launch_bounds__(256) void k_clip(NormArgs a) {
 
 template <int P, int G>
 hipError_t go(bool bits8, const AdamwArgs& a, hipStream_t s) {
-    const dim3 grid(adamw_grid(a.ntiles)), block(256);
+    const dim3 grid(a.ntiles), block(256);
     if (bits8) {
         if (a.stream_past) hipLaunchKernelGGL((k_adamw<P, G, true, true>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((k_adamw<P, G, true, false>), grid, block, 0, s, a);
@@ -733,8 +779,6 @@ hipError_t go_grad(int grad, bool bits8, const AdamwArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Four tiles, one per wave, to a workgroup.
-int adamw_grid(int64_t ntiles) { return (int)((ntiles + 3) / 4); }
 // At most two workgroups of eight waves on each of the 256 CUs (302M bf16
 // elements: 103 us; with 16 waves 108, with 1024 workgroups of four 105).
 int norm_grid(int64_t ntiles) {

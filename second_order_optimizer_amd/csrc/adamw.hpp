@@ -24,10 +24,10 @@ struct AdamwTensor {
     int32_t id, pad_;        // index in the plan's list
 };
 
-// Some runs of one tensor, the work of one wave.
+// Up to kTileRuns runs of one tensor, the work of one workgroup of four waves.
+constexpr int kTileRuns = 8;
 struct AdamwTile {
-    int32_t tensor;          // index into the tensor table
-    int32_t nruns;
+    int32_t tensor, pad_;    // index into the tensor table
     int64_t run0;            // first run within the tensor
 };
 
@@ -106,7 +106,6 @@ __host__ __device__ inline uint32_t mix32_rest(uint32_t x) {   // after the firs
 }
 __host__ __device__ inline uint32_t mix32(uint32_t x) { return mix32_rest(x ^ (x >> 16)); }
 
-int adamw_grid(int64_t ntiles);
 int norm_grid(int64_t ntiles);
 
 hipError_t launch_adamw(int param, int grad, bool bits8, const AdamwArgs& a, hipStream_t s);
