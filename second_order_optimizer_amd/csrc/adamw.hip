@@ -476,10 +476,10 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
 // spread the accesses over more of the memory's pages at once.  fp32 moments,
 // 302M fp32 elements: 1367 us with 4, 1385 with 6, 1434 (up to 1520) with 8.
 // 8-bit moments need more for the arithmetic, 302M / 60M bf16 elements: 805 /
-// 192 us with 3, 730 / 177 with 4, 690 / 165 with 6, 715 (up to 752) / 164
-// with 7.
+// 192 us with 3, 730 / 177 with 4, 695 / 161 with 5, 745 / 158 with 6, 755 /
+// 157 with 7.
 template <int P, int G, bool S8, bool NT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, S8 ? 6 : 4))) void k_adamw(AdamwArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, S8 ? 5 : 4))) void k_adamw(AdamwArgs a) {
     // field by field: a copy of the whole struct, its padding included, went
     // through LDS and cost 14 us at 256 workgroups
     AdamwClock* clock = a.clocks + blockIdx.x;
