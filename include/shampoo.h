@@ -459,7 +459,8 @@ typedef struct {
 
 /* Plan for the gradients of n_tensors tensors.  Host only.  Errors:
  * SHAMPOO_E_ARG (null, n_tensors < 1, numel < 0, unknown dtype, reserved not
- * 0), SHAMPOO_E_UNSUPPORTED (numel above 2^38), SHAMPOO_E_NOMEM. */
+ * 0), SHAMPOO_E_UNSUPPORTED (more than 2^26 pieces of 1024 elements of one
+ * tensor), SHAMPOO_E_NOMEM. */
 int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
                             shampoo_gradnorm_t** out);
 /* Bytes of device state (tables, partial sums, the record); 256-byte aligned,
@@ -487,9 +488,11 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
 /* out <- coef g, in fp32, for every bound output, by the record of the last
  * shampoo_gradnorm_compute; 0 everywhere when the norm was not finite, so
  * that a Shampoo step that takes these gradients adds nothing to its
- * statistics.  Errors: SHAMPOO_E_STATE, SHAMPOO_E_HIP. */
+ * statistics.  Errors: SHAMPOO_E_STATE (also no outputs bound, or no norm
+ * computed yet), SHAMPOO_E_HIP. */
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream);
-/* Device address of the record (inside the state buffer).  Host only. */
+/* Device address of the record (inside the state buffer; all zero until the
+ * first shampoo_gradnorm_compute).  Host only. */
 int shampoo_gradnorm_record(const shampoo_gradnorm_t* h, const shampoo_clip_record** dev_record);
 void shampoo_gradnorm_destroy(shampoo_gradnorm_t* h);
 
@@ -506,7 +509,8 @@ typedef struct {
 typedef struct {
     int64_t numel;
     int32_t param_type;   /* SHAMPOO_F32, or SHAMPOO_BF16: the weight is the bf16 value plus
-                             a 16-bit remainder in the state, together its fp32 value    */
+                             a 16-bit remainder in the state, together its fp32 value
+                             (zero the remainders when weights are replaced)             */
     int32_t grad_type;    /* shampoo_dtype */
     int32_t state_bits;   /* 32: fp32 moments; 8: e4m3 codes of m and of sqrt(v) with one
                              fp32 scale per run of 256 elements each                     */
@@ -530,8 +534,8 @@ typedef struct {
 /* Plan for n_tensors tensors.  Host only.  Errors: SHAMPOO_E_ARG (null,
  * n_tensors < 1, numel < 0, a beta outside [0, 1), eps out of range,
  * weight_decay or lr_scale negative or not finite, unknown types, state_bits
- * not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16 weights, numel
- * above 2^38), SHAMPOO_E_NOMEM. */
+ * not 8 or 32, reserved not 0), SHAMPOO_E_UNSUPPORTED (fp16 weights; 2^24 or
+ * more workgroups of 2048 elements of one tensor), SHAMPOO_E_NOMEM. */
 int shampoo_adamw_create(const shampoo_adamw_config* cfg, int32_t n_tensors,
                          const shampoo_adamw_tensor* tensors, shampoo_adamw_t** out);
 int shampoo_adamw_get_layout(const shampoo_adamw_t* h, shampoo_adamw_layout* out);

@@ -127,6 +127,7 @@ class GradNorm(_Bound):
         at = _P()
         _check(L.shampoo_gradnorm_record(h, ctypes.byref(at)), "shampoo_gradnorm_record")
         self.record_ptr = at.value
+        self.computed = False
         off = at.value - self.state.data_ptr()
         #: [norm, coefficient] of the last compute, on the device
         self.record = self.state[off:off + 8].view(self.torch.float32)
@@ -147,6 +148,7 @@ class GradNorm(_Bound):
     def compute(self, max_norm: float = float("inf"), grad_scale: float = 1.0):
         """Norm and coefficient of the bound gradients into ``record``."""
         self._call(lib().shampoo_gradnorm_compute, max_norm, grad_scale)
+        self.computed = True
 
     def clip_into(self):
         """The clipped gradients into the bound outputs."""
@@ -196,8 +198,8 @@ class AdamW(_Bound):
             if lr.dtype != self.torch.float32 or lr.numel() != 1 or lr.device != self.device:
                 raise ValueError(f"lr must be a number or one fp32 element on {self.device}")
             dev_lr, lr = lr.data_ptr(), 0.0
-        if clip is not None and clip.device != self.device:
-            raise ValueError(f"clip must be on {self.device}")
+        if clip is not None and (clip.device != self.device or not clip.computed):
+            raise ValueError(f"clip must be on {self.device} and have computed a norm")
         self._call(lib().shampoo_adamw_step, lr, dev_lr, None if clip is None else clip.record_ptr)
 
     def set_step(self, t: int):
@@ -218,7 +220,8 @@ class AdamW(_Bound):
         """The moments and remainders of every tensor, one after another in
         whole runs of 256 elements: "m", "v" in fp32; "m8", "s8" as e4m3
         values of m and sqrt(v) with their scales "m_scale", "s_scale" (one per
-        run); "rem", what bf16 weights lack of their fp32 value."""
+        run); "rem", what bf16 weights lack of their fp32 value (zero it when
+        the weights are replaced)."""
         lay, t = self.layout, self.torch
         out = {}
         if lay.runs32:

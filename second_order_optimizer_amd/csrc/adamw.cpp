@@ -23,7 +23,7 @@ using namespace shampoo;
 
 namespace {
 
-constexpr int64_t kMaxNumel = (int64_t)1 << 38;    // runs of a tensor stay below 2^31
+constexpr int64_t kMaxNumel = (int64_t)1 << 36;
 // A step over more than this passes the caches by: its data would not be there
 // at the next step, and what they hold of the program's stays (three plans in
 // turn of 16M fp32 elements: 80 us, 92 through the caches; of 4M: 22 us, 19
@@ -33,7 +33,8 @@ constexpr int64_t kCacheBytes = (int64_t)96 << 20;
 // them again (60M bf16 elements, norm and 8-bit step: 168 us, 174 past it).
 constexpr int64_t kGradCacheBytes = (int64_t)192 << 20;
 constexpr double kMinEps = 0x1p-100;               // sqrt(v) c + eps is a normal number
-constexpr int64_t kMaxTiles = (int64_t)1 << 30;
+constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in a launch
+constexpr int64_t kMaxPieces = (int64_t)1 << 26;         // pieces of a norm plan, likewise
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int64_t runs_of(int64_t numel) { return (numel + kRun - 1) / kRun; }
@@ -92,7 +93,7 @@ struct shampoo_gradnorm_s {
     int64_t off_table = 0, off_tiles = 0, off_partials = 0, off_tickets = 0, off_record = 0;
     size_t total = 0;
     unsigned char* arena = nullptr;
-    bool bound = false, grads_bound = false;
+    bool bound = false, grads_bound = false, outs_bound = false, computed = false;
     int device = -1;
 };
 
@@ -359,7 +360,7 @@ int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
             return SHAMPOO_E_ARG;
         if (d.numel > kMaxNumel) return SHAMPOO_E_UNSUPPORTED;
         tiles += d.numel / kNormPiece + 1;
-        if (tiles > kMaxTiles) return SHAMPOO_E_UNSUPPORTED;
+        if (tiles > kMaxPieces) return SHAMPOO_E_UNSUPPORTED;
     }
     shampoo_gradnorm_s* h = new (std::nothrow) shampoo_gradnorm_s();
     if (!h) return SHAMPOO_E_NOMEM;
@@ -406,7 +407,7 @@ int shampoo_gradnorm_bind_state(shampoo_gradnorm_t* h, void* dev_state, size_t b
     if (!h || !dev_state || !aligned_to(dev_state, 256)) return SHAMPOO_E_ARG;
     if (bytes < h->total) return SHAMPOO_E_STATE;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    h->bound = h->grads_bound = false;
+    h->bound = h->grads_bound = h->outs_bound = h->computed = false;
     if (hipGetDevice(&h->device) != hipSuccess) return SHAMPOO_E_HIP;
     h->arena = static_cast<unsigned char*>(dev_state);
     int rc = status_of(hipMemsetAsync(h->arena, 0, h->total, s));
@@ -473,6 +474,7 @@ int shampoo_gradnorm_bind_grads(shampoo_gradnorm_t* h, const void* const* grads,
         if (rc) return rc;
     }
     h->grads_bound = true;
+    h->outs_bound = outs != nullptr;
     return SHAMPOO_OK;
 }
 
@@ -485,12 +487,14 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
     a.stream_past = h->grad_bytes > kGradCacheBytes;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
-    return status_of(launch_norm(a, static_cast<hipStream_t>(stream)));
+    const int rc = status_of(launch_norm(a, static_cast<hipStream_t>(stream)));
+    h->computed |= rc == SHAMPOO_OK;
+    return rc;
 }
 
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream) {
     if (!h) return SHAMPOO_E_ARG;
-    if (!h->bound || !h->grads_bound || !on_device(h->device)) return SHAMPOO_E_STATE;
+    if (!h->bound || !h->outs_bound || !h->computed || !on_device(h->device)) return SHAMPOO_E_STATE;
     if (h->tiles.empty()) return SHAMPOO_OK;
     return status_of(launch_clip(norm_args(h), static_cast<hipStream_t>(stream)));
 }

@@ -259,7 +259,8 @@ __device__ __forceinline__ f32x4 decode4(uint32_t w) {
 // offset, in bits that the shift does not reach.  ANY: the run holds values
 // below 2^-6 of e4m3's range or not finite.
 template <bool ANY, bool NT>
-__device__ __forceinline__ void encode_run(const f32x4* m, const f32x4* root, float mi, float si, uint32_t start, uint64_t m8, uint64_t s8, uint32_t lo) {
+__device__ __forceinline__ void encode_run(const f32x4* m, const f32x4* root, float mi, float si,
+                                           uint32_t start, uint64_t m8, uint64_t s8, uint32_t lo) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint32_t h[4], mw = 0, sw = 0;

@@ -54,6 +54,11 @@ def test_adamw_create_refuses_config(field, value):
     assert create([A.tensor(10)], c)[0] == E_ARG
 
 
+def test_plans_past_a_launch():
+    assert create([A.tensor(1 << 34), A.tensor(1 << 34), A.tensor(1)])[0] == E_UNSUPPORTED
+    assert create_norm([S.GradDesc(1 << 36, 0, 0), S.GradDesc(1, 0, 0)])[0] == E_UNSUPPORTED
+
+
 def test_nulls_and_unbound_handles():
     L = S.lib()
     assert create([])[0] == E_ARG

@@ -732,6 +732,13 @@ def test_refusals():
     norm.bind([p[1]])
     with pytest.raises(S.ShampooError):
         norm.compute(0.0)
+    with pytest.raises(ValueError):
+        opt.step(1e-3, clip=norm)                         # no norm computed yet
+    norm.compute(1.0)
+    with pytest.raises(S.ShampooError):
+        norm.clip_into()                                  # no outputs bound
+    norm.bind([p[1]], [torch.empty(4, device="cuda")])
+    norm.clip_into()
     two = A.GradNorm([(4, "f32"), (4, "f32")])
     x = torch.zeros(16, device="cuda")
     two.bind([x[:4], x[4:8]], [x[:4], x[8:12]])
