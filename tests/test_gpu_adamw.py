@@ -554,6 +554,61 @@ def test_captured_and_replayed():
                 assert np.array_equal(a[key], b[key], equal_nan=True), (k, key)
 
 
+def test_two_graphs_of_the_same_handles():
+    """One graph with the clip and one without, in turn, against eager steps."""
+    sizes = (700, 40000)
+    make = lambda: Run([A.tensor(n, state_bits=b, weight_decay=0.1) for n in sizes for b in (32, 8)], 19)
+    eager, run = make(), make()
+    norms = [A.GradNorm([(s.numel, "f32") for s in r.specs]) for r in (eager, run)]
+    for n, r in zip(norms, (eager, run)):
+        n.bind(r.grads)
+
+    def go(k, clip):
+        r = (eager, run)[k]
+        if clip:
+            norms[k].compute(0.5)
+        r.opt.step(1e-3, clip=norms[k] if clip else None)
+
+    for k in (0, 1):
+        go(k, True)
+    graphs = []
+    for clip in (True, False):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            go(1, clip)
+        graphs.append(g)
+    for k in (0, 1, 1, 0, 1, 0):
+        for i in range(len(eager.specs)):
+            x = torch.from_numpy(eager.draw(i)).cuda()
+            eager.grads[i].copy_(x)
+            run.grads[i].copy_(x)
+        go(0, k == 0)
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    for a, b in zip(eager.read(), run.read()):
+        for key in a:
+            assert np.array_equal(a[key], b[key]), key
+
+
+def test_gradients_of_new_addresses_every_step():
+    """Gradients that are allocated anew, bound and freed at every step."""
+    specs = [A.tensor(n, param="bf16", state_bits=b) for n in (5, 3000, 90001) for b in (32, 8)]
+    a, b = Run(specs, 6), Run(specs, 6)
+    for _ in range(4):
+        new = [torch.from_numpy(a.draw(i)).to("cuda", torch.bfloat16) for i in range(len(specs))]
+        for g, x in zip(b.grads, new):
+            g.copy_(x)
+        a.opt.bind(grads=new)
+        a.opt.step(1e-3)
+        del new, x
+        b.opt.step(1e-3)
+    for x, y in zip(a.read(), b.read()):
+        for k in x:
+            if k != "g":
+                assert np.array_equal(x[k], y[k]), k
+
+
 def test_another_stream():
     a, b = Run([A.tensor(50000, state_bits=8)], 1), Run([A.tensor(50000, state_bits=8)], 1)
     s = torch.cuda.Stream()
