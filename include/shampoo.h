@@ -488,7 +488,7 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
 /* out <- coef g, in fp32, for every bound output, by the record of the last
  * shampoo_gradnorm_compute; 0 everywhere when the norm was not finite, so
  * that a Shampoo step that takes these gradients adds nothing to its
- * statistics.  Errors: SHAMPOO_E_STATE (also no outputs bound, or no norm
+ * statistics.  The output of an absent gradient stays as it is.  Errors: SHAMPOO_E_STATE (also no outputs bound, or no norm
  * computed yet), SHAMPOO_E_HIP. */
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream);
 /* Device address of the record (inside the state buffer; all zero until the

@@ -64,7 +64,9 @@ class _Bound:
         self._types = (torch.float32, torch.bfloat16, torch.float16)
 
         # the current stream of a device as a number, without a Stream object
-        self._stream = torch._C._cuda_getCurrentRawStream
+        # where torch offers that (0.1 us instead of 1.9)
+        self._stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                               lambda index: torch.cuda.current_stream(index).cuda_stream)
         self._current = torch.cuda.current_device
 
     def _call(self, fn, *args):

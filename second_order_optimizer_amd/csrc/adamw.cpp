@@ -24,14 +24,12 @@ using namespace shampoo;
 namespace {
 
 constexpr int64_t kMaxNumel = (int64_t)1 << 36;
-// A step over more than this passes the caches by: its data would not be there
-// at the next step, and what they hold of the program's stays (three plans in
-// turn of 16M fp32 elements: 80 us, 92 through the caches; of 4M: 22 us, 19
-// through them).  Of the 256 MiB last-level cache a program leaves a step part.
+// A step or a norm over more than this passes the caches by: its data would
+// not be there at the next step, and what they hold of the program's stays.
+// Three plans in turn of 16M fp32 elements: 78 us, 90 through the caches; of
+// 4M: 21 us, 19 through them; the norm of 302M bf16 elements: 92 us, 103
+// through them.  Of the 256 MiB last-level cache a program leaves a step part.
 constexpr int64_t kCacheBytes = (int64_t)96 << 20;
-// Gradients up to this stay there between their norm and the step that reads
-// them again (60M bf16 elements, norm and 8-bit step: 168 us, 174 past it).
-constexpr int64_t kGradCacheBytes = (int64_t)192 << 20;
 constexpr double kMinEps = 0x1p-100;               // sqrt(v) c + eps is a normal number
 constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in a launch
 constexpr int64_t kMaxPieces = (int64_t)1 << 26;         // pieces of a norm plan, likewise
@@ -365,7 +363,7 @@ int shampoo_gradnorm_create(int32_t n_tensors, const shampoo_grad_desc* tensors,
     shampoo_gradnorm_s* h = new (std::nothrow) shampoo_gradnorm_s();
     if (!h) return SHAMPOO_E_NOMEM;
     // twice the work for one reading of the tables once every wave has several
-    // (302M bf16 elements: 103 us, 108 with four)
+    // (302M bf16 elements: 92 us, 93 with one piece, 99 with four)
     h->pieces = tiles >= 8 * 8192 ? 2 : 1;
     try {
         const int64_t per_tile = (int64_t)h->pieces * kNormPiece;
@@ -483,8 +481,7 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
         return SHAMPOO_E_ARG;
     if (!h->bound || !h->grads_bound || !on_device(h->device)) return SHAMPOO_E_STATE;
     NormArgs a = norm_args(h);
-    // (302M bf16 elements: 93 us past the caches, 103 through them)
-    a.stream_past = h->grad_bytes > kGradCacheBytes;
+    a.stream_past = h->grad_bytes > kCacheBytes;
     a.max_norm = max_norm;
     a.grad_scale = grad_scale;
     const int rc = status_of(launch_norm(a, static_cast<hipStream_t>(stream)));

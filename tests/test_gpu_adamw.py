@@ -689,7 +689,7 @@ def test_norm(offset, scale, grad_scale):
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_norm_past_the_caches(kind):
-    """More than 192 MiB of gradients; one value in each of a few places."""
+    """More gradients than the caches hold; one value in each of a few places."""
     n = (204 << 20) // (4 if kind == "f32" else 2) + 77
     g = torch.zeros(n + 3, dtype=TORCH[kind], device="cuda")[3:]
     for i, k in enumerate((0, 1023, 1024, n // 2, n - 78, n - 1)):
