@@ -194,7 +194,10 @@ __device__ __forceinline__ float reciprocal(float d) {
 }
 // m/d rounded to nearest: the quotient by the rounded reciprocal is within
 // one unit, and its remainder, exact in one fma, decides (Markstein 1990).
-// d: positive, normal, below 2^126.
+// d: positive, normal, below 2^126.  m: 0, or at least 2^-100 in magnitude, so
+// that the remainder's last place (2^-47 of m) is one of fp32, with a quotient
+// that is normal and finite: of smaller ones one in ten at m = 2^-125 would be
+// off by its last place.
 __device__ __forceinline__ float quotient(float m, float d) {
     const float y = reciprocal(d);
     const float q = m * y;
@@ -205,6 +208,8 @@ __device__ __forceinline__ float quotient(float m, float d) {
 // and every exponent of that range, counted on the card).  NaN for v that is
 // not finite.
 constexpr uint32_t kRootLow = 0x0F800000u;   // 2^-96
+constexpr float kQuoLow = 0x1p-100f;         // the least |m| of `quotient`
+constexpr uint32_t kQuoHigh = 0x67000000u;   // 2^79, which the root of kRootLow takes to 2^127
 __device__ __forceinline__ float near_root(float v) {
     const float y = __builtin_amdgcn_rsqf(__uint_as_float(umax(__float_as_uint(v), kRootLow)));
     const float r = v * y;
@@ -338,7 +343,11 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
             v[j] = ld<NT>(lane_at<const f32x4>(vb, 4 * lo, 512 * j));
         }
     }
-    uint32_t vmin = 0xFFFFFFFFu;
+    // the largest magnitude of m as the largest signed and the largest unsigned
+    // of its bits: positive and negative values, NaN above all; the least that
+    // is not 0 as the least of twice its bits - 1
+    int mpos = 0;
+    uint32_t mneg = 0, mlow = 0xFFFFFFFFu, vmin = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         f32x4 x = widen4<G>(graw[j]);
@@ -358,10 +367,14 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
             m[j][q] = m[j][q] * a.b1 + x[q] * a.c1;
             v[j][q] = v[j][q] * a.b2 + (x[q] * x[q]) * a.c2;
             vmin = umin(vmin, __float_as_uint(v[j][q]));
+            const uint32_t b = __float_as_uint(m[j][q]);
+            mpos = mpos > (int)b ? mpos : (int)b;
+            mneg = umax(mneg, b);
+            mlow = umin(mlow, (b << 1) - 1u);
         }
     }
     f32x4 root[2], quo[2];
-    uint32_t smax = 0;
+    uint32_t smax = 0, mmax = umax((uint32_t)mpos, mneg & 0x7FFFFFFFu);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -369,8 +382,10 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
             root[j][q] = near_root(v[j][q]);
             smax = umax(smax, __float_as_uint(root[j][q]));
         }
-    if (__any(vmin < kRootLow || smax > kFinite)) {
-        // zeros, tiny second moments and those that are not finite
+    // the least m whose quotient by the lane's largest divisor is normal
+    const float least = fmaxf((__uint_as_float(smax) * root_c + a.eps) * 0x1p-125f, kQuoLow);
+    if (__any(vmin < kRootLow || smax > kFinite || mlow < (__float_as_uint(least) << 1) - 1u || mmax >= kQuoHigh)) {
+        // second moments that are 0, tiny or not finite, and tiny or huge m
         smax = 0;
         for (int j = 0; j < 2; ++j)
             for (int q = 0; q < 4; ++q) {
@@ -425,22 +440,14 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
         }
     }
     if constexpr (S8) {
-        // the largest magnitude of m as the largest signed and the largest
-        // unsigned of its bits: positive and negative values, NaN above all
-        int mpos = 0;
-        uint32_t mneg = 0;
-        float mlow = __builtin_inff(), slow = __builtin_inff();
+        float mleast = __builtin_inff(), sleast = __builtin_inff();
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int b = (int)__float_as_uint(m[j][q]);
-                mpos = mpos > b ? mpos : b;
-                mneg = umax(mneg, (uint32_t)b);
-                mlow = fminf(mlow, fabsf(m[j][q]));
-                slow = fminf(slow, root[j][q]);
+                mleast = fminf(mleast, fabsf(m[j][q]));
+                sleast = fminf(sleast, root[j][q]);
             }
-        uint32_t mmax = umax((uint32_t)mpos, mneg & 0x7FFFFFFFu);
         uint32_t top = half_max2(mmax, smax);
         const bool odd = __any(top > kFinite);
         if (odd) {   // the scales are those of the finite values
@@ -464,7 +471,7 @@ __device__ __forceinline__ void step_runs(const AdamwArgs& a, const AdamwTensor&
         const uint64_t e0 = (uint64_t)run * kRun;
         uint32_t start = (key + (uint32_t)(e0 >> 32) * 0x85157AF5u) ^ ((uint32_t)e0 | lo);
         start ^= start >> 16;
-        if (__any(mlow * mi < 0x1p-6f || slow * si < 0x1p-6f) || odd)
+        if (__any(mleast * mi < 0x1p-6f || sleast * si < 0x1p-6f) || odd)
             encode_run<true, NT>(m, root, mi, si, start, mb, vb, lo);
         else
             encode_run<false, NT>(m, root, mi, si, start, mb, vb, lo);

@@ -804,6 +804,80 @@ def test_refusals():
         A.AdamW([A.tensor(4)], device="cpu")
 
 
+# ------------------------------------------------- roots and quotients, counted
+RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
+
+
+class Still:
+    """A step that changes no moments: betas of 1 in fp32, corrections of 1 (no
+    decay, zero gradients), so that p = -m / (sqrt(v) + 2^-100)."""
+
+    def __init__(self, n):
+        self.p, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+        almost = 1 - 2.0 ** -53
+        self.opt = A.AdamW([A.tensor(n)], A.make_config(beta1=almost, beta2=almost, eps=2.0 ** -100))
+        self.opt.set_step(1 << 62)
+        self.opt.bind([self.p], [g])
+        held = self.opt.state_tensors()
+        self.m, self.v = held["m"], held["v"]
+
+    def quotients(self):
+        self.p.zero_()
+        self.opt.step(1.0)
+        return -self.p
+
+
+def plain_quotients(m, v):
+    zero = np.float32(0)
+    with np.errstate(all="ignore"):
+        return -(zero - (zero + m / (np.sqrt(v) + np.float32(2.0 ** -100))))
+
+
+def signed(rng, x):
+    return (x * rng.choice([-1.0, 1.0], x.shape)).astype(np.float32)
+
+
+@pytest.mark.parametrize("m_range,v_range", [
+    ((-149, -100), (-40, 0)),       # what a few hundred zero gradients leave of m
+    ((-110, -90), (-96, -80)), ((-110, -60), (60, 128)), ((-30, 60), (-96, -60)), ((60, 127.9), (-96, -40)),
+    ((60, 127.9), (60, 128)), ((-149, 127.9), (-149, 128))])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_quotients_over_the_range(m_range, v_range, mixed):
+    """Small and large quotients bit for bit, in waves of their own and among
+    elements of an everyday size."""
+    n = 64 * RUN_PAIR
+    rng = np.random.default_rng(1)
+    m = signed(rng, 2.0 ** rng.uniform(*m_range, n))
+    v = np.minimum(2.0 ** rng.uniform(*v_range, n), 3.4e38).astype(np.float32)
+    if mixed:
+        usual = rng.random(n) < 0.9
+        m[usual] = signed(rng, rng.uniform(1e-4, 1e-3, usual.sum()))
+        v[usual] = rng.uniform(1e-8, 1e-6, usual.sum())
+    s = Still(n)
+    s.m.copy_(torch.from_numpy(m))
+    s.v.copy_(torch.from_numpy(v))
+    got, want = s.quotients().cpu().numpy(), plain_quotients(m, v)
+    assert np.array_equal(got.view(np.uint32), want.view(np.uint32)), np.flatnonzero(got != want)[:5]
+
+
+def test_an_element_does_not_depend_on_its_neighbours():
+    """The same tiny m beside an everyday element and beside a second moment of
+    zero."""
+    n = 4 * RUN_PAIR
+    rng = np.random.default_rng(2)
+    m = signed(rng, 2.0 ** rng.uniform(-126, -118, n))
+    v = rng.uniform(1e-8, 1e-6, n).astype(np.float32)
+    got = []
+    for beside in (1e-7, 0.0):
+        v[::RUN_PAIR], m[::RUN_PAIR] = beside, 0.0
+        s = Still(n)
+        s.m.copy_(torch.from_numpy(m))
+        s.v.copy_(torch.from_numpy(v))
+        got.append(s.quotients().cpu().numpy())
+    keep = np.arange(n) % RUN_PAIR != 0
+    assert np.array_equal(got[0][keep].view(np.uint32), got[1][keep].view(np.uint32))
+
+
 # ------------------------------------------------------------ as they are used
 def test_shampoo_and_adamw_under_one_norm():
     """A model's end of step: bf16 gradients under one norm, matrices on Shampoo
