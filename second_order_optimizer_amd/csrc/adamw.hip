@@ -187,7 +187,8 @@ __device__ __forceinline__ void half_both(float v, float& first, float& second) 
 
 // 1/d rounded to nearest, for normal d and 1/d: one Newton step on the
 // hardware's reciprocal (equal to 1/d for every significand and every
-// exponent from -125 to 125, counted on the card).
+// exponent from -125 to 125; the tests count those of the divisors that second
+// moments from 2^-96 on give).
 __device__ __forceinline__ float reciprocal(float d) {
     const float y = __builtin_amdgcn_rcpf(d);
     return __builtin_fmaf(__builtin_fmaf(-d, y, 1.f), y, y);
@@ -205,7 +206,7 @@ __device__ __forceinline__ float quotient(float m, float d) {
 }
 // sqrt(v) rounded to nearest for v = 0 and 2^-96 <= v < infinity: one
 // correction of v / sqrt(v) (equal to the rounded root for every significand
-// and every exponent of that range, counted on the card).  NaN for v that is
+// and every exponent of that range, which the tests count).  NaN for v that is
 // not finite.
 constexpr uint32_t kRootLow = 0x0F800000u;   // 2^-96
 constexpr float kQuoLow = 0x1p-100f;         // the least |m| of `quotient`

@@ -833,8 +833,39 @@ def plain_quotients(m, v):
         return -(zero - (zero + m / (np.sqrt(v) + np.float32(2.0 ** -100))))
 
 
+def short_waves(m, root, v, c, eps):
+    """Which waves' elements are all in the range of the corrected estimates."""
+    with np.errstate(all="ignore"):
+        d = root.astype(np.float64) * c + eps
+        a = np.abs(m.astype(np.float64))
+        ok = np.isfinite(v) & (v >= 2.0 ** -96) & (a < 2.0 ** 79) & ((a == 0) | (a >= np.maximum(2.0 ** -100, d * 2.0 ** -124)))
+    return ok.reshape(-1, RUN_PAIR).all(1)
+
+
 def signed(rng, x):
     return (x * rng.choice([-1.0, 1.0], x.shape)).astype(np.float32)
+
+
+def test_every_root_and_divisor():
+    """Every significand at every exponent from 2^-96 on as a second moment,
+    each under an m of its own: root and quotient are the rounded ones.  (The
+    roots of [1, 4) take every significand of a divisor.)"""
+    n = 1 << 24
+    s = Still(n)
+    rng = np.random.default_rng(0)
+    significand = torch.arange(n, dtype=torch.int32, device="cuda")
+    m = signed(rng, rng.uniform(1, 2, n))
+    m[rng.random(n) < 0.05] = 0.0
+    s.m.copy_(torch.from_numpy(m))
+    for e in range(-96, 128, 2):
+        s.v.copy_((significand + ((e + 127) << 23)).view(torch.float32))
+        got = s.quotients()
+        # fp64 has more than twice the bits, so that rounding twice is rounding once
+        want = (s.m.double() / s.v.double().sqrt().float().double()).float()
+        bad = torch.nonzero(got != want).flatten().cpu().numpy()
+        if bad.size:
+            v = s.v.cpu().numpy()[bad]
+            assert np.array_equal(got.cpu().numpy()[bad], plain_quotients(m[bad], v)), (e, bad.size)
 
 
 @pytest.mark.parametrize("m_range,v_range", [
@@ -876,6 +907,50 @@ def test_an_element_does_not_depend_on_its_neighbours():
         got.append(s.quotients().cpu().numpy())
     keep = np.arange(n) % RUN_PAIR != 0
     assert np.array_equal(got[0][keep].view(np.uint32), got[1][keep].view(np.uint32))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lo,hi", [(-8, 0), (-40, -20), (40, 63)])
+def test_every_rounding_of_short_waves(lo, hi, bits):
+    """Steps of waves whose elements all take the corrected estimates and, with
+    8-bit moments, the hardware's conversion: bit for bit the fp32 formula.
+    Signs stay and a wave's gradients are within a factor of 8, so that no value
+    falls below 2^-6 of e4m3's range (448 / 2^-6 is 2^14.8)."""
+    waves = 64
+    n = waves * RUN_PAIR
+    rng = np.random.default_rng(64 + hi)
+    size = np.repeat(2.0 ** rng.uniform(lo, hi - 1, waves), RUN_PAIR)
+    sign = rng.choice([-1.0, 1.0], n)
+    eps = 2.0 ** -60
+    h = O.Hyper(lr=1e-3, weight_decay=0.1, eps=eps)
+    opt = A.AdamW([A.tensor(n, state_bits=bits, weight_decay=0.1)], A.make_config(eps=eps, seed=9))
+    w = rng.standard_normal(n).astype(np.float32)
+    m, v = np.zeros(n, np.float32), np.zeros(n, np.float32)
+    p, g = torch.from_numpy(w.copy()).cuda(), torch.zeros(n, device="cuda")
+    opt.bind([p], [g])
+    held = opt.state_tensors()
+    same = lambda a, b: np.array_equal(np.asarray(a).view(np.uint32), np.asarray(b).view(np.uint32))
+    for t in (1, 2, 3):
+        x = (sign * size * rng.uniform(0.25, 2, n)).astype(np.float32)
+        g.copy_(torch.from_numpy(x))
+        opt.step(h.lr)
+        w, m, root, v = O.step32(w, x, m, v, t, h)
+        assert short_waves(m, root, v, 1 / np.sqrt(1 - h.beta2 ** t), eps).all()
+        assert same(p.cpu().numpy(), w), t
+        if bits == 32:
+            assert same(held["m"].cpu().numpy(), m) and same(held["v"].cpu().numpy(), v)
+            continue
+        rm, rs = O.random_bits(9, t, 0, np.arange(n))
+        for value, r, code, scale, pos in ((m, rm, "m8", "m_scale", False), (root, rs, "s8", "s_scale", True)):
+            c, s = O.codes32(value, r, pos)
+            assert np.all(np.abs(value).reshape(-1, 256) > 1.001 * 2.0 ** -6 * s[:, None])
+            assert same(held[scale].cpu().numpy(), s), (t, scale)
+            assert np.array_equal(held[code].view(torch.uint8).cpu().numpy(), c), (t, code)
+        spread = lambda k: np.repeat(held[k].cpu().numpy(), 256)
+        dec = lambda k: O.decode(held[k].view(torch.uint8).cpu().numpy()).astype(np.float32)
+        m = dec("m8") * spread("m_scale")
+        root = dec("s8") * spread("s_scale")
+        v = root * root
 
 
 # ------------------------------------------------------------ as they are used
