@@ -137,6 +137,10 @@ void plan_adamw(shampoo_adamw_s* h) {
         }
         for (int64_t k = 0; k < n; k += kTileRuns) g->tiles.push_back({(int32_t)i, 0, k});
     }
+    if (h->groups.empty()) {   // nothing but empty tensors: a workgroup that counts steps
+        h->groups.emplace_back();
+        h->groups[0].tiles.push_back({0, 0, 0});
+    }
     int64_t at = 0;
     const auto take = [&at](int64_t bytes) {
         const int64_t o = at;
@@ -147,7 +151,6 @@ void plan_adamw(shampoo_adamw_s* h) {
         g.off_clocks = (int64_t)h->nclocks * (int64_t)sizeof(AdamwClock);
         h->nclocks += (int)g.tiles.size();
     }
-    h->nclocks = std::max(h->nclocks, 1);
     h->lay.off_clock = take((int64_t)h->nclocks * (int64_t)sizeof(AdamwClock));
     h->off_table = take((int64_t)(h->table.size() * sizeof(AdamwTensor)));
     for (auto& g : h->groups) g.off_tiles = take((int64_t)(g.tiles.size() * sizeof(AdamwTile)));

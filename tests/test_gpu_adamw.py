@@ -804,6 +804,30 @@ def test_refusals():
         A.AdamW([A.tensor(4)], device="cpu")
 
 
+def test_empty_tensors_count_steps():
+    """A plan whose tensors are all empty counts its steps like any other, and
+    skips those whose norm is not finite."""
+    nothing = torch.empty(0, device="cuda")
+    opt = A.AdamW([A.tensor(0), A.tensor(0, state_bits=8)])
+    opt.bind([nothing, None], [nothing, None])
+    g = torch.ones(4, device="cuda")
+    norm = A.GradNorm([(4, "f32")])
+    norm.bind([g])
+    for t, x in ((1, 1.0), (2, 1.0), (2, float("nan")), (3, 1.0)):
+        g[0] = x
+        norm.compute(1.0)
+        opt.step(1e-3, clip=norm)
+        assert int(opt.t) == t
+    opt.set_step(7)
+    opt.step(1e-3)
+    assert int(opt.t) == 8
+    # an address that is given for nothing is not read
+    at = (S._P * 2)(g.data_ptr(), g.data_ptr())
+    assert S.lib().shampoo_adamw_bind_tensors(opt.h, at, at, None) == 0
+    opt.step(1e-3)
+    assert int(opt.t) == 9 and g[1:].tolist() == [1.0, 1.0, 1.0]
+
+
 # ------------------------------------------------- roots and quotients, counted
 RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
 
