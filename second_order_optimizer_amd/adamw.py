@@ -249,6 +249,8 @@ class AdamW(_Bound):
         if set(saved) != {"t", *held} or any(saved[k].shape != x.shape or saved[k].dtype != x.dtype
                                              for k, x in held.items()):
             raise ValueError("the state is of other tensors")
+        if saved["t"] < 0:      # before anything is changed
+            raise ValueError("a number of steps is not negative")
         for k, x in held.items():
             x.copy_(saved[k])
         self.set_step(saved["t"])

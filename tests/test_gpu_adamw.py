@@ -828,6 +828,17 @@ def test_empty_tensors_count_steps():
     assert int(opt.t) == 9 and g[1:].tolist() == [1.0, 1.0, 1.0]
 
 
+def test_refused_state_changes_nothing():
+    run = Run([A.tensor(n, param="bf16", state_bits=b) for n in (300, 1000) for b in (32, 8)], 3, t0=5)
+    before = {k: x.view(torch.uint8).clone() for k, x in run.opt.state_tensors().items()}
+    saved = {k: x.zero_() if k != "t" else -1 for k, x in run.opt.state_dict().items()}
+    with pytest.raises(ValueError):
+        run.opt.load_state_dict(saved)
+    assert int(run.opt.t) == 5
+    for k, x in run.opt.state_tensors().items():
+        assert torch.equal(x.view(torch.uint8), before[k]), k
+
+
 # ------------------------------------------------- roots and quotients, counted
 RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
 
