@@ -453,7 +453,8 @@ typedef struct {
                             past the range of fp32)                                      */
     float coef;          /* grad_scale min(1, max_norm / n): the factor of a clipped
                             gradient; 0 when n is not finite                             */
-    int32_t nonfinite;   /* 1: n is not finite (some gradient is infinite or NaN)        */
+    int32_t nonfinite;   /* 1: n is not finite (some gradient is infinite or NaN), or not yet
+                            computed                                                     */
     int32_t reserved;
 } shampoo_clip_record;
 
@@ -491,8 +492,10 @@ int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad
  * statistics.  The output of an absent gradient stays as it is.  Errors: SHAMPOO_E_STATE (also no outputs bound, or no norm
  * computed yet), SHAMPOO_E_HIP. */
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream);
-/* Device address of the record (inside the state buffer; all zero until the
- * first shampoo_gradnorm_compute).  Host only. */
+/* Device address of the record (inside the state buffer).  Until the first
+ * shampoo_gradnorm_compute has run on the device -- one that was captured runs
+ * with its graph -- norm and coef are 0 and nonfinite is 1, so that a step
+ * that reads it changes nothing.  Host only. */
 int shampoo_gradnorm_record(const shampoo_gradnorm_t* h, const shampoo_clip_record** dev_record);
 void shampoo_gradnorm_destroy(shampoo_gradnorm_t* h);
 

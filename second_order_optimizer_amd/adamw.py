@@ -133,7 +133,7 @@ class GradNorm(_Bound):
         off = at.value - self.state.data_ptr()
         #: [norm, coefficient] of the last compute, on the device
         self.record = self.state[off:off + 8].view(self.torch.float32)
-        #: 1 where that norm is not finite, on the device
+        #: 1 where that norm is not finite, or none has run yet, on the device
         self.nonfinite = self.state[off + 8:off + 12].view(self.torch.int32)
 
     def bind(self, grads, outs=None):

@@ -421,6 +421,11 @@ int shampoo_gradnorm_bind_state(shampoo_gradnorm_t* h, void* dev_state, size_t b
                                       h->tiles.size() * sizeof(NormTile), hipMemcpyHostToDevice, s));
         if (rc) return rc;
     }
+    // no norm yet (a captured one only runs with its graph): a step that reads
+    // the record changes nothing
+    const ClipRecord none{0.f, 0.f, 1, 0};
+    rc = status_of(hipMemcpyAsync(h->arena + h->off_record, &none, sizeof none, hipMemcpyHostToDevice, s));
+    if (rc) return rc;
     rc = status_of(hipStreamSynchronize(s));
     if (rc) return rc;
     h->bound = true;

@@ -839,6 +839,32 @@ def test_refused_state_changes_nothing():
         assert torch.equal(x.view(torch.uint8), before[k]), k
 
 
+def test_a_norm_that_has_not_run_skips_the_step():
+    """Between the capture of a norm and the first replay its record holds no
+    coefficient: steps that read it change nothing, clipped gradients are 0."""
+    run = Run([A.tensor(n, state_bits=b, weight_decay=0.1) for n in (300, 1000) for b in (32, 8)], 3, t0=5)
+    out = [torch.full_like(g, 7.0) for g in run.grads]
+    norm = A.GradNorm([(s.numel, "f32") for s in run.specs])
+    norm.bind(run.grads, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm.compute(1.0)
+    before = run.read()
+    run.opt.step(1e-3, clip=norm)
+    norm.clip_into()
+    assert int(run.opt.t) == 5 and not any(bool(o.any()) for o in out)
+    for a, b in zip(before, run.read()):
+        for k in a:
+            assert np.array_equal(a[k], b[k]), k
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        before = run.read()
+        run.opt.step(1e-3, clip=norm)
+        run.check(before, 1e-3, float(norm.record[1]))
+
+
 # ------------------------------------------------- roots and quotients, counted
 RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
 
