@@ -546,6 +546,17 @@ int shampoo_adamw_get_layout(const shampoo_adamw_t* h, shampoo_adamw_layout* out
  * for fp32 weights).  Host only. */
 int shampoo_adamw_tensor_runs(const shampoo_adamw_t* h, int32_t tensor, int64_t* state_run,
                               int64_t* rem_run);
+/* What t counts in the corrections 1 - beta^t of a step.  0, as created: the
+ * handle's steps, also those in which a tensor had no gradient: one whose first
+ * gradient comes late is corrected as if its moments were as old as the handle
+ * (after 1000 steps with betas 0.9 and 0.999 its first update is 2.5 lr' and
+ * not lr', much later 3.2 lr').  1: the steps in which the tensor had a
+ * gradient.  Before shampoo_adamw_bind_state; host only.  Errors:
+ * SHAMPOO_E_ARG (neither 0 nor 1), SHAMPOO_E_STATE (state already bound). */
+int shampoo_adamw_set_counting(shampoo_adamw_t* h, int32_t per_tensor);
+/* Byte offset in the state buffer of a tensor's own count (int64; equal to the
+ * handle's while that is what counts), -1 for an empty tensor.  Host only. */
+int shampoo_adamw_tensor_count(const shampoo_adamw_t* h, int32_t tensor, int64_t* offset);
 /* Attach the state (layout.total bytes, 256-byte aligned) and initialise it:
  * moments and remainders 0, no steps done.  Waits for that.  Errors:
  * SHAMPOO_E_ARG, SHAMPOO_E_STATE (too small), SHAMPOO_E_HIP. */
@@ -558,19 +569,23 @@ int shampoo_adamw_bind_state(shampoo_adamw_t* h, void* dev_state, size_t bytes, 
  * SHAMPOO_E_HIP, SHAMPOO_E_NOMEM. */
 int shampoo_adamw_bind_tensors(shampoo_adamw_t* h, void* const* params, const void* const* grads,
                                void* stream);
-/* Set the number of steps done (t >= 0), e.g. after restoring the moments. */
+/* Set the number of steps done (t >= 0), e.g. after restoring the moments: the
+ * handle's and every tensor's own. */
 int shampoo_adamw_set_step(shampoo_adamw_t* h, int64_t t, void* stream);
+/* Set every tensor's own count (n_tensors values >= 0) where those are what
+ * counts (SHAMPOO_E_STATE otherwise); the handle's stays. */
+int shampoo_adamw_set_tensor_steps(shampoo_adamw_t* h, const int64_t* steps, void* stream);
 /* One step of every bound tensor:
  *   x = coef g;  m = beta1 m + (1 - beta1) x;  v = beta2 v + (1 - beta2) x^2
  *   p = p - lr' (weight_decay p + (m / (1 - beta1^t)) /
  *                (sqrt(v / (1 - beta2^t)) + eps)),      lr' = lr lr_scale
- * t counting from 1.  lr: the learning rate, unless dev_lr is given: one fp32
+ * t counting from 1 (whose steps: shampoo_adamw_set_counting).  lr: the learning rate, unless dev_lr is given: one fp32
  * on the device, read when the step runs.  dev_clip: NULL (coef 1), or a
  * record of shampoo_gradnorm_compute: coef is its coefficient, and where it
  * says nonfinite the step leaves weights, moments and t as they are.
  * 8-bit moments are rounded to the code below or above at random, with the
  * probabilities that make the mean of what is stored the value itself; the
- * random bits are a hash of (seed, t, tensor index, element).  A positive
+ * random bits are a hash of (seed, the handle's t, tensor index, element).  A positive
  * sqrt(v) is never stored as 0; a value that is not finite is stored as NaN
  * and does not touch its run's scale.
  * Errors: SHAMPOO_E_ARG (lr not finite, a misaligned pointer), SHAMPOO_E_STATE

@@ -22,7 +22,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
-from typing import Dict, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 from .shampoo import (AdamWConfig, AdamWLayout, AdamWTensor, GradDesc, ShampooError, _check, _P,
                       lib)
@@ -158,10 +158,15 @@ class GradNorm(_Bound):
 
 
 class AdamW(_Bound):
-    """One AdamW step over many tensors (specs from ``tensor``)."""
+    """One AdamW step over many tensors (specs from ``tensor``).
+
+    per_tensor_steps: the bias corrections count the steps in which a tensor had
+    a gradient, for tensors whose gradients start late or come now and then.
+    Otherwise they count the handle's steps, and a first gradient after a
+    thousand of them moves its tensor by 2.5 lr."""
 
     def __init__(self, tensors: Sequence[AdamWTensor], cfg: Optional[AdamWConfig] = None,
-                 device="cuda"):
+                 device="cuda", per_tensor_steps: bool = False):
         L = lib()
         self._destroy = L.shampoo_adamw_destroy
         self.tensors = list(tensors)
@@ -171,6 +176,8 @@ class AdamW(_Bound):
         _check(L.shampoo_adamw_create(ctypes.byref(self.cfg), len(self.tensors), descs,
                                       ctypes.byref(h)), "shampoo_adamw_create")
         self.h = h
+        self.per_tensor_steps = bool(per_tensor_steps)
+        _check(L.shampoo_adamw_set_counting(h, int(self.per_tensor_steps)), "shampoo_adamw_set_counting")
         self.layout = AdamWLayout()
         _check(L.shampoo_adamw_get_layout(h, ctypes.byref(self.layout)), "shampoo_adamw_get_layout")
         self._open(device)
@@ -205,8 +212,28 @@ class AdamW(_Bound):
         self._call(lib().shampoo_adamw_step, lr, dev_lr, None if clip is None else clip.record_ptr)
 
     def set_step(self, t: int):
-        """Set the number of steps done, e.g. after restoring the moments."""
+        """Set the number of steps done, the handle's and every tensor's own,
+        e.g. after restoring the moments."""
         self._call(lib().shampoo_adamw_set_step, t)
+
+    def set_tensor_steps(self, steps: Sequence[int]):
+        """Set every tensor's own number of steps (with per_tensor_steps)."""
+        if len(steps) != len(self.tensors):
+            raise ValueError(f"{len(steps)} counts for a plan of {len(self.tensors)}")
+        self._call(lib().shampoo_adamw_set_tensor_steps, (ctypes.c_int64 * len(self.tensors))(*steps))
+
+    def tensor_steps(self) -> List[int]:
+        """Every tensor's own number of steps, 0 for an empty one (waits for the
+        GPU)."""
+        at = []
+        for i in range(len(self.tensors)):
+            off = ctypes.c_int64()
+            _check(lib().shampoo_adamw_tensor_count(self.h, i, ctypes.byref(off)),
+                   "shampoo_adamw_tensor_count")
+            at.append(off.value)
+        index = self.torch.tensor([max(o, 0) // 8 for o in at], device=self.device)
+        got = self.state.view(self.torch.int64)[index].tolist()
+        return [k if o >= 0 else 0 for k, o in zip(got, at)]
 
     # ---- views into the state buffer
     def _view(self, off, count, dtype):
@@ -241,16 +268,23 @@ class AdamW(_Bound):
     def state_dict(self) -> Dict[str, object]:
         """Copies of the moments and remainders, and the number of steps done
         (waits for the GPU)."""
-        return {"t": int(self.t), **{k: x.clone() for k, x in self.state_tensors().items()}}
+        out = {"t": int(self.t), **{k: x.clone() for k, x in self.state_tensors().items()}}
+        if self.per_tensor_steps:
+            out["tensor_steps"] = self.tensor_steps()
+        return out
 
     def load_state_dict(self, saved: Dict[str, object]):
         """Restore what ``state_dict`` of a handle with the same tensors gave."""
         held = self.state_tensors()
-        if set(saved) != {"t", *held} or any(saved[k].shape != x.shape or saved[k].dtype != x.dtype
-                                             for k, x in held.items()):
-            raise ValueError("the state is of other tensors")
-        if saved["t"] < 0:      # before anything is changed
+        names = {"t", *held} | ({"tensor_steps"} if self.per_tensor_steps else set())
+        counts = saved.get("tensor_steps", [])
+        if (set(saved) != names or len(counts) != len(self.tensors) * self.per_tensor_steps
+                or any(saved[k].shape != x.shape or saved[k].dtype != x.dtype for k, x in held.items())):
+            raise ValueError("the state is of other tensors, or counts their steps in another way")
+        if any(t < 0 for t in (saved["t"], *counts)):      # before anything is changed
             raise ValueError("a number of steps is not negative")
         for k, x in held.items():
             x.copy_(saved[k])
         self.set_step(saved["t"])
+        if self.per_tensor_steps:
+            self.set_tensor_steps(counts)

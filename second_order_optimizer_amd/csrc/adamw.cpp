@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -67,6 +68,11 @@ struct Group {
     int64_t off_tiles = 0, off_clocks = 0;
 };
 
+// The step counters of a tensor's workgroups.
+struct Clocks {
+    int first = 0, n = 0;
+};
+
 }  // namespace
 
 struct shampoo_adamw_s {
@@ -74,6 +80,8 @@ struct shampoo_adamw_s {
     std::vector<shampoo_adamw_tensor> desc;
     std::vector<AdamwTensor> table;
     std::vector<Group> groups;
+    std::vector<Clocks> clocks;   // of each tensor
+    bool per_tensor = false;
     shampoo_adamw_layout lay{};
     int64_t off_table = 0;
     int nclocks = 0;
@@ -99,11 +107,11 @@ namespace {
 
 AdamwClock clock_at(const shampoo_adamw_config& c, int64_t t) {
     AdamwClock k{};
-    k.t = t;
-    k.b1t = std::pow(c.beta1, (double)(t + 1));
-    k.b2t = std::pow(c.beta2, (double)(t + 1));
-    k.inv1 = 1.0 / (1.0 - k.b1t);
-    k.inv_root2 = (float)(1.0 / std::sqrt(1.0 - k.b2t));
+    k.t = k.k = t;
+    k.b1k = std::pow(c.beta1, (double)(t + 1));
+    k.b2k = std::pow(c.beta2, (double)(t + 1));
+    k.inv1 = 1.0 / (1.0 - k.b1k);
+    k.inv_root2 = (float)(1.0 / std::sqrt(1.0 - k.b2k));
     return k;
 }
 
@@ -147,9 +155,14 @@ void plan_adamw(shampoo_adamw_s* h) {
         at = round_up(at + bytes, 256);
         return o;
     };
+    h->clocks.resize(h->desc.size());
     for (auto& g : h->groups) {
         g.off_clocks = (int64_t)h->nclocks * (int64_t)sizeof(AdamwClock);
-        h->nclocks += (int)g.tiles.size();
+        for (const auto& t : g.tiles) {   // those of one tensor follow one another
+            Clocks& c = h->clocks[t.tensor];
+            if (c.n++ == 0) c.first = h->nclocks;
+            ++h->nclocks;
+        }
     }
     h->lay.off_clock = take((int64_t)h->nclocks * (int64_t)sizeof(AdamwClock));
     h->off_table = take((int64_t)(h->table.size() * sizeof(AdamwTensor)));
@@ -167,9 +180,12 @@ void plan_adamw(shampoo_adamw_s* h) {
     h->lay.total = at;
 }
 
+AdamwClock* clocks_of(shampoo_adamw_s* h) {
+    return reinterpret_cast<AdamwClock*>(h->arena + h->lay.off_clock);
+}
+
 int fill_clocks(shampoo_adamw_s* h, int64_t t, hipStream_t s) {
-    return status_of(launch_adamw_clock(reinterpret_cast<AdamwClock*>(h->arena + h->lay.off_clock),
-                                        h->nclocks, clock_at(h->cfg, t), s));
+    return status_of(launch_adamw_clock(clocks_of(h), h->nclocks, clock_at(h->cfg, t), 1 | 2, s));
 }
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -236,6 +252,22 @@ int shampoo_adamw_tensor_runs(const shampoo_adamw_t* h, int32_t tensor, int64_t*
     const bool rem = h->desc[tensor].param_type == SHAMPOO_BF16;
     if (state_run) *state_run = h->table[tensor].state_run;
     if (rem_run) *rem_run = rem ? h->table[tensor].rem_run : -1;
+    return SHAMPOO_OK;
+}
+
+int shampoo_adamw_set_counting(shampoo_adamw_t* h, int32_t per_tensor) {
+    if (!h || (per_tensor != 0 && per_tensor != 1)) return SHAMPOO_E_ARG;
+    if (h->bound) return SHAMPOO_E_STATE;
+    h->per_tensor = per_tensor == 1;
+    return SHAMPOO_OK;
+}
+
+int shampoo_adamw_tensor_count(const shampoo_adamw_t* h, int32_t tensor, int64_t* offset) {
+    if (!h || !offset || tensor < 0 || tensor >= (int32_t)h->table.size()) return SHAMPOO_E_ARG;
+    const Clocks& c = h->clocks[tensor];
+    *offset = c.n ? h->lay.off_clock + (int64_t)c.first * (int64_t)sizeof(AdamwClock) +
+                        (int64_t)offsetof(AdamwClock, k)
+                  : -1;
     return SHAMPOO_OK;
 }
 
@@ -309,6 +341,21 @@ int shampoo_adamw_set_step(shampoo_adamw_t* h, int64_t t, void* stream) {
     return fill_clocks(h, t, static_cast<hipStream_t>(stream));
 }
 
+int shampoo_adamw_set_tensor_steps(shampoo_adamw_t* h, const int64_t* steps, void* stream) {
+    if (!h || !steps) return SHAMPOO_E_ARG;
+    if (!h->per_tensor || !h->bound || !on_device(h->device)) return SHAMPOO_E_STATE;
+    for (size_t i = 0; i < h->desc.size(); ++i)
+        if (steps[i] < 0) return SHAMPOO_E_ARG;
+    for (size_t i = 0; i < h->desc.size(); ++i) {
+        const Clocks& c = h->clocks[i];
+        if (!c.n) continue;
+        const int rc = status_of(launch_adamw_clock(clocks_of(h) + c.first, c.n, clock_at(h->cfg, steps[i]), 2,
+                                                    static_cast<hipStream_t>(stream)));
+        if (rc) return rc;
+    }
+    return SHAMPOO_OK;
+}
+
 int shampoo_adamw_step(shampoo_adamw_t* h, double lr, const float* dev_lr,
                        const shampoo_clip_record* dev_clip, void* stream) {
     if (!h || !std::isfinite(lr) || !aligned_to(dev_lr, 4) || !aligned_to(dev_clip, 16))
@@ -338,6 +385,7 @@ int shampoo_adamw_step(shampoo_adamw_t* h, double lr, const float* dev_lr,
     a.s_scale = reinterpret_cast<float*>(h->arena + h->lay.off_s_scale);
     a.rem = reinterpret_cast<int16_t*>(h->arena + h->lay.off_rem);
     a.stream_past = h->step_bytes > kCacheBytes;
+    a.per_tensor = h->per_tensor;
     for (const auto& g : h->groups) {
         a.tiles = reinterpret_cast<const AdamwTile*>(h->arena + g.off_tiles);
         a.ntiles = (int32_t)g.tiles.size();

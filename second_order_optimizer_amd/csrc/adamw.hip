@@ -492,8 +492,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, S8 ? 5 :
     // field by field: a copy of the whole struct, its padding included, went
     // through LDS and cost 14 us at 256 workgroups
     AdamwClock* clock = a.clocks + blockIdx.x;
-    const int64_t t = clock->t;
-    const double b1t = clock->b1t, b2t = clock->b2t, inv1 = clock->inv1;
+    const int64_t t = clock->t, k = clock->k;
+    const double b1k = clock->b1k, b2k = clock->b2k, inv1 = clock->inv1;
     const float root_c = clock->inv_root2;
     float coef = 1.f;
     if (a.clip) {
@@ -517,18 +517,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, S8 ? 5 :
     }
     __syncthreads();   // every wave has read the clock
     if (threadIdx.x == 0) {
-        const double n1 = b1t * a.beta1, n2 = b2t * a.beta2;
         clock->t = t + 1;
-        clock->b1t = n1;
-        clock->b2t = n2;
+        if (a.per_tensor && !ts.g_ptr) return;   // no step of this tensor
+        const double n1 = b1k * a.beta1, n2 = b2k * a.beta2;
+        clock->k = k + 1;
+        clock->b1k = n1;
+        clock->b2k = n2;
         clock->inv1 = 1.0 / (1.0 - n1);
         clock->inv_root2 = (float)(1.0 / sqrt(1.0 - n2));
     }
 }
 
-__global__ __launch_bounds__(256) void k_adamw_clock(AdamwClock* clocks, int n, AdamwClock c) {
+__global__ __launch_bounds__(256) void k_adamw_clock(AdamwClock* clocks, int n, AdamwClock c, int which) {
     const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i < n) clocks[i] = c;
+    if (i >= n) return;
+    if (which & 1) clocks[i].t = c.t;
+    if (which & 2) {
+        clocks[i].k = c.k;
+        clocks[i].b1k = c.b1k;
+        clocks[i].b2k = c.b2k;
+        clocks[i].inv1 = c.inv1;
+        clocks[i].inv_root2 = c.inv_root2;
+    }
 }
 
 // The pointers travel as kernel arguments, so that a captured graph holds
@@ -799,8 +809,8 @@ hipError_t launch_adamw(int param, int grad, bool bits8, const AdamwArgs& a, hip
                            : go_grad<DT_BF16>(grad, bits8, a, s);
 }
 
-hipError_t launch_adamw_clock(AdamwClock* clocks, int n, const AdamwClock& c, hipStream_t s) {
-    hipLaunchKernelGGL(k_adamw_clock, dim3((n + 255) / 256), dim3(256), 0, s, clocks, n, c);
+hipError_t launch_adamw_clock(AdamwClock* clocks, int n, const AdamwClock& c, int which, hipStream_t s) {
+    hipLaunchKernelGGL(k_adamw_clock, dim3((n + 255) / 256), dim3(256), 0, s, clocks, n, c, which);
     return hipGetLastError();
 }
 

@@ -36,10 +36,11 @@ struct AdamwTile {
 // whole step, replayed launches count on, and no workgroup waits for another.
 struct AdamwClock {
     int64_t t;               // steps done
-    double b1t, b2t;         // beta^(t + 1)
-    double inv1;             // 1 / (1 - beta1^(t + 1))
-    float inv_root2;         // 1 / sqrt(1 - beta2^(t + 1))
-    int32_t pad_[7];
+    int64_t k;               // steps that the corrections count: t, or the tensor's own
+    double b1k, b2k;         // beta^(k + 1)
+    double inv1;             // 1 / (1 - beta1^(k + 1))
+    float inv_root2;         // 1 / sqrt(1 - beta2^(k + 1))
+    int32_t pad_[5];
 };
 static_assert(sizeof(AdamwClock) == 64, "one clock per 64 bytes");
 
@@ -61,6 +62,7 @@ struct AdamwArgs {
     uint32_t seed_mixed;
     int32_t ntiles;
     int32_t stream_past;         // the step touches more than the caches hold
+    int32_t per_tensor;          // the corrections count a tensor's own steps
     float *m, *v;                // fp32 moments
     unsigned char *m8, *s8;      // 8-bit moments: e4m3 of m and sqrt(v)
     float *m_scale, *s_scale;
@@ -109,7 +111,8 @@ __host__ __device__ inline uint32_t mix32(uint32_t x) { return mix32_rest(x ^ (x
 int norm_grid(int64_t ntiles);
 
 hipError_t launch_adamw(int param, int grad, bool bits8, const AdamwArgs& a, hipStream_t s);
-hipError_t launch_adamw_clock(AdamwClock* clocks, int n, const AdamwClock& c, hipStream_t s);
+// which: 1 the step count, 2 the corrections' count and factors
+hipError_t launch_adamw_clock(AdamwClock* clocks, int n, const AdamwClock& c, int which, hipStream_t s);
 hipError_t launch_adamw_bind(AdamwTensor* tensors, int first, int n, const PtrBatch& b, int which,
                              hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);

@@ -143,6 +143,9 @@ SIGNATURES = {
     "shampoo_adamw_bind_state": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "shampoo_adamw_bind_tensors": (ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P]),
     "shampoo_adamw_set_step": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
+    "shampoo_adamw_set_counting": (ctypes.c_int, [_P, ctypes.c_int32]),
+    "shampoo_adamw_tensor_count": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
+    "shampoo_adamw_set_tensor_steps": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int64), _P]),
     "shampoo_adamw_step": (ctypes.c_int, [_P, ctypes.c_double, _P, _P, _P]),
     "shampoo_adamw_destroy": (None, [_P]),
     "shampoo_destroy": (None, [_P]),

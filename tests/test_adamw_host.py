@@ -141,6 +141,42 @@ def test_plan_layout(sizes):
     S.lib().shampoo_adamw_destroy(h)
 
 
+def test_counting_of_steps():
+    """Each tensor has a count of its own in the clocks' region, an empty one
+    none."""
+    L = S.lib()
+    sizes = [5, 0, 2049, 300, 1, 70000]
+    rc, h = create([A.tensor(n, state_bits=(8, 32)[i % 2]) for i, n in enumerate(sizes)])
+    assert rc == 0
+    lay = S.AdamWLayout()
+    assert L.shampoo_adamw_get_layout(h, ctypes.byref(lay)) == 0
+    at = []
+    for i, n in enumerate(sizes):
+        off = ctypes.c_int64()
+        assert L.shampoo_adamw_tensor_count(h, i, ctypes.byref(off)) == 0
+        if n == 0:
+            assert off.value == -1
+            continue
+        assert off.value % 64 == 8 and off.value >= lay.off_clock
+        at.append(off.value)
+    clocks = sum(-(-n // 2048) for n in sizes)
+    assert len(set(at)) == len(at) and max(at) < lay.off_clock + 64 * clocks
+    off = ctypes.c_int64()
+    assert L.shampoo_adamw_tensor_count(h, len(sizes), ctypes.byref(off)) == E_ARG
+    assert L.shampoo_adamw_tensor_count(h, -1, ctypes.byref(off)) == E_ARG
+    assert L.shampoo_adamw_tensor_count(h, 0, None) == E_ARG
+    assert L.shampoo_adamw_tensor_count(None, 0, ctypes.byref(off)) == E_ARG
+    steps = (ctypes.c_int64 * len(sizes))()
+    assert L.shampoo_adamw_set_tensor_steps(h, steps, None) == E_STATE       # the handle's are counted
+    for bad in (-1, 2):
+        assert L.shampoo_adamw_set_counting(h, bad) == E_ARG
+    assert L.shampoo_adamw_set_counting(None, 1) == E_ARG
+    assert L.shampoo_adamw_set_counting(h, 1) == 0
+    assert L.shampoo_adamw_set_tensor_steps(h, steps, None) == E_STATE       # no state bound
+    assert L.shampoo_adamw_set_tensor_steps(h, None, None) == E_ARG
+    L.shampoo_adamw_destroy(h)
+
+
 # ------------------------------------------------------------ the oracle itself
 def test_oracle_codes_are_e4m3():
     torch = pytest.importorskip("torch")

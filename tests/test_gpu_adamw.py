@@ -865,6 +865,98 @@ def test_a_norm_that_has_not_run_skips_the_step():
         run.check(before, 1e-3, float(norm.record[1]))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_first_gradient_after_a_thousand_steps(bits):
+    """From zero moments: the first update is lr where the tensor's own steps
+    are counted, and 2.5 lr where the handle's are."""
+    n, lr = 1000, 1e-3
+    g = np.random.default_rng(3).standard_normal(n).astype(np.float32)
+    for own, t in ((True, 1), (False, 1001)):
+        p = torch.zeros(n, device="cuda")
+        opt = A.AdamW([A.tensor(n, state_bits=bits)], per_tensor_steps=own)
+        opt.set_step(1000)
+        if own:
+            opt.set_tensor_steps([0])
+        opt.bind([p], [torch.from_numpy(g).cuda()])
+        opt.step(lr)
+        zero = np.zeros(n)
+        want, _, _, _, err = O.step(zero, g.astype(np.float64), zero, zero, t, O.Hyper(lr=lr))[:5]
+        assert np.all(np.abs(np64(p) - want) <= err)
+        # |g| / (|g| + eps) is 1 to 1e-8 / |g|; 0.1 / sqrt(0.001 / (1 - 0.999^1001)) = 2.515
+        size = np.abs(np64(p))[np.abs(g) > 0.1] / lr
+        assert np.allclose(size, 1.0 if own else 2.515, rtol=1e-3)
+        assert int(opt.t) == 1001 and opt.tensor_steps() == [t]
+
+
+def test_tensors_count_their_own_steps():
+    """Gradients that come now and then: each tensor is corrected as by a handle
+    of its own that only steps when there is one, eager and replayed, with steps
+    whose norm is not finite between; a saved state goes on alike."""
+    kinds = [(n, p, b) for n in (700, 5000) for p in ("f32", "bf16") for b in (32, 8)] + [(0, "f32", 32)]
+    specs = [A.tensor(n, param=p, grad="f32", state_bits=b, weight_decay=0.1) for n, p, b in kinds]
+    rng = np.random.default_rng(8)
+    start = [torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda().to(TORCH[p]) for n, p, _ in kinds]
+    grads = [torch.zeros(n, device="cuda") for n, _, _ in kinds]
+    every = A.AdamW(specs, per_tensor_steps=True)
+    weights = [w.clone() for w in start]
+    every.bind(weights, grads)
+    single, alone = [A.AdamW([s]) for s in specs], [w.clone() for w in start]
+    for o, w, g in zip(single, alone, grads):
+        o.bind([w], [g])
+    norm = A.GradNorm([(n, "f32") for n, _, _ in kinds])
+    norm.bind(grads)
+    counts, t = [0] * len(kinds), 0
+    graph = None
+    for k in range(14):
+        if k == 4:      # the state goes on in another handle
+            saved, old = every.state_dict(), every
+            every = A.AdamW(specs, per_tensor_steps=True)
+            every.load_state_dict(saved)
+            every.bind(weights, grads)
+            assert every.tensor_steps() == old.tensor_steps() == counts
+        present = [(k + i) % 3 != 0 or k >= 10 for i in range(len(kinds))]
+        bad = k in (2, 12)
+        for i, g in enumerate(grads):
+            g.normal_(0, 1e-2)
+        if bad:
+            grads[1][3] = float("inf")
+        norm.compute()
+        if k < 10:
+            every.bind(grads=[g if here else None for g, here in zip(grads, present)])
+            every.step(1e-3, clip=norm)
+        else:
+            if graph is None:
+                every.bind(grads=grads)
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    every.step(1e-3, clip=norm)
+            graph.replay()
+        t += not bad
+        for i, here in enumerate(present):
+            if here:
+                single[i].step(1e-3, clip=norm)
+                counts[i] += not bad and kinds[i][0] > 0
+        torch.cuda.synchronize()
+        assert int(every.t) == t and every.tensor_steps() == counts
+        for i, (n, _, b) in enumerate(kinds):
+            # the rounding of 8-bit moments goes by the handle's step: equal until it has been read
+            if b == 32 or counts[i] <= 1:
+                assert torch.equal(weights[i], alone[i]), (k, i)
+    with pytest.raises(ValueError):
+        A.AdamW(specs).load_state_dict(every.state_dict())
+    with pytest.raises(ValueError):
+        every.load_state_dict(A.AdamW(specs).state_dict())
+    with pytest.raises(ValueError):
+        every.set_tensor_steps([1])
+    with pytest.raises(S.ShampooError):
+        every.set_tensor_steps([-1] + counts[1:])
+    with pytest.raises(S.ShampooError):
+        single[0].set_tensor_steps([1])
+    assert every.tensor_steps() == counts
+    assert S.lib().shampoo_adamw_set_counting(every.h, 0) == -2       # its state is bound
+
+
 # ------------------------------------------------- roots and quotients, counted
 RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
 
