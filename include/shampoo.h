@@ -488,9 +488,12 @@ int shampoo_gradnorm_bind_grads(shampoo_gradnorm_t* h, const void* const* grads,
 int shampoo_gradnorm_compute(shampoo_gradnorm_t* h, double max_norm, double grad_scale, void* stream);
 /* out <- coef g, in fp32, for every bound output, by the record of the last
  * shampoo_gradnorm_compute; 0 everywhere when the norm was not finite, so
- * that a Shampoo step that takes these gradients adds nothing to its
- * statistics.  The output of an absent gradient stays as it is.  Errors: SHAMPOO_E_STATE (also no outputs bound, or no norm
- * computed yet), SHAMPOO_E_HIP. */
+ * that nothing that is not finite reaches the state of a Shampoo step that
+ * takes these gradients.  That step is not skipped by it, as an AdamW step is
+ * by its dev_clip: statistics with beta2 < 1 decay, momentum moves the weights,
+ * its t counts on.  A caller who wants it skipped reads `nonfinite` first.  The
+ * output of an absent gradient stays as it is.  Errors: SHAMPOO_E_STATE (also
+ * no outputs bound, or no norm computed yet), SHAMPOO_E_HIP. */
 int shampoo_gradnorm_clip_into(shampoo_gradnorm_t* h, void* stream);
 /* Device address of the record (inside the state buffer).  Until the first
  * shampoo_gradnorm_compute has run on the device -- one that was captured runs

@@ -13,7 +13,10 @@ bits, and the global gradient norm whose clip coefficient it reads.
         opt.step(lr=1e-3, clip=norm)
 
 Beside Shampoo, GradNorm takes the gradients of both optimizers and
-``clip_into`` writes the fp32 ones that Shampoo.step takes.  ``bind``,
+``clip_into`` writes the fp32 ones that Shampoo.step takes: zeros where the norm
+is not finite, with which a Shampoo step still decays its statistics (beta2 < 1)
+and moves weights by its momentum; to leave that step out as AdamW does, read
+``nonfinite`` first.  ``bind``,
 ``compute``, ``clip_into`` and ``step`` neither wait for the GPU nor copy to it,
 and can be captured into a graph; what is bound or captured stays alive, and is
 used by one stream at a time.  It raises if the library has not been built --

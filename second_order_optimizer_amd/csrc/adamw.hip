@@ -759,8 +759,8 @@ __device__ __forceinline__ void tile_clip(const NormTensor& ts, int64_t first, i
     }
 }
 
-// The clipped gradients in fp32; zeros when the norm is not finite, so that a
-// step that takes them adds nothing to its statistics.
+// The clipped gradients in fp32; zeros when the norm is not finite, so that
+// nothing else reaches the statistics of a step that takes them.
 __global__ __launch_bounds__(256) void k_clip(NormArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
