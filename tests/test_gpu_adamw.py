@@ -957,6 +957,39 @@ def test_tensors_count_their_own_steps():
     assert S.lib().shampoo_adamw_set_counting(every.h, 0) == -2       # its state is bound
 
 
+def test_captured_clip():
+    """Norm and clipped copies in a graph, one of them in place: every replay is
+    the eager result, with a gradient that is not finite among them."""
+    kinds = [(700, "f32"), (40000, "bf16"), (5000, "f16"), (300, "f32")]
+    rng = np.random.default_rng(5)
+    sets = []
+    for _ in range(2):
+        grads = [torch.zeros(n, dtype=TORCH[k], device="cuda") for n, k in kinds]
+        outs = [grads[0]] + [torch.zeros(n, device="cuda") for n, _ in kinds[1:]]
+        norm = A.GradNorm(kinds)
+        norm.bind(grads, outs)
+        sets.append((grads, outs, norm))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sets[1][2].compute(1.0)
+        sets[1][2].clip_into()
+    for k in range(5):
+        for i, (n, kind) in enumerate(kinds):
+            x = torch.from_numpy(rng.standard_normal(n)).cuda().to(TORCH[kind])
+            if k == 2 and i == 1:
+                x[5] = float("inf")
+            for grads, _, _ in sets:
+                grads[i].copy_(x)
+        sets[0][2].compute(1.0)
+        sets[0][2].clip_into()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(sets[1][2].nonfinite) == (k == 2)
+        for a, b in zip(sets[0][1] + [sets[0][2].record], sets[1][1] + [sets[1][2].record]):
+            assert torch.equal(a, b), k
+
+
 # ------------------------------------------------- roots and quotients, counted
 RUN_PAIR = 512          # elements of a wave: the two runs that take one path together
 
