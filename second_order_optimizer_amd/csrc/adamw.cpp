@@ -30,6 +30,11 @@ constexpr int64_t kMaxNumel = (int64_t)1 << 36;
 // Three plans in turn of 16M fp32 elements: 78 us, 90 through the caches; of
 // 4M: 21 us, 19 through them; the norm of 302M bf16 elements: 92 us, 103
 // through them.  Of the 256 MiB last-level cache a program leaves a step part.
+// What reads the gradients after their norm gains or loses by it (norm and what
+// follows, through the caches / past them): clip_into of 120 and 250 MB of fp32
+// 70 / 67 and 143 / 131 us; a step of bf16 weights with 8-bit moments 161 / 159
+// and 336 / 332; one with fp32 moments, fp32 gradients 148 / 161 and 308 / 336,
+// bf16 ones 266 / 283 and 555 / 592.  A norm's plan does not know what follows.
 constexpr int64_t kCacheBytes = (int64_t)96 << 20;
 constexpr double kMinEps = 0x1p-100;               // sqrt(v) c + eps is a normal number
 constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in a launch
