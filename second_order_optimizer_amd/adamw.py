@@ -204,7 +204,9 @@ class AdamW(_Bound):
     def step(self, lr, clip: Optional[GradNorm] = None):
         """One step.  lr: a number, or one fp32 element on the device that the
         step reads when it runs.  clip: scale the gradients by the coefficient
-        of its last compute, and skip the step where its norm is not finite."""
+        of its last compute, and skip the step where its norm is not finite.
+        The gradients are those before clipping: not ones that clip_into has
+        scaled in place."""
         dev_lr = None
         if isinstance(lr, self.torch.Tensor):
             if lr.dtype != self.torch.float32 or lr.numel() != 1 or lr.device != self.device:
