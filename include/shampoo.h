@@ -597,6 +597,167 @@ int shampoo_adamw_step(shampoo_adamw_t* h, double lr, const float* dev_lr,
                        const shampoo_clip_record* dev_clip, void* stream);
 void shampoo_adamw_destroy(shampoo_adamw_t* h);
 
+/* ================================================== layers in 8 bits
+ * What stands around the product of a layer whose weights the steps above own:
+ * the product itself in 8-bit floating point with a scale for each block of
+ * 128, forward and for both gradients; the root-mean-square norm that feeds it,
+ * with the residual's addition, and its gradient; activations and gradients
+ * turned into 8 bits; and 8-bit copies of many weights, refreshed after a step.
+ *
+ *   y  = x W^T    matmul8(x by rows, W by rows)
+ *   dx = dy W     matmul8(dy by rows, W's transpose by rows)
+ *   dW = dy^T x   matmul8(dy's transpose, x's transpose), fp32, added up over
+ *                 micro-batches: the gradient that shampoo_step reads
+ *
+ * The conventions of the first-order operators hold; wide matrices are
+ * row-major with `pitch` elements from row to row (at least the columns, unless
+ * there is one row at most) and may start at any element.  These calls keep no
+ * state between them, run on the device that is current, allocate nothing, and
+ * can be captured; the outputs must not overlap an input or each other but
+ * where a call says so (SHAMPOO_E_ARG).  A dimension of 0 is allowed where
+ * nothing else is said: outputs without elements are left alone.  Results are
+ * bit for bit repeatable. */
+
+typedef enum { SHAMPOO_E4M3 = 0, SHAMPOO_E5M2 = 1 } shampoo_format8;
+
+/* An 8-bit matrix.  Each row is cut into blocks of 128 values under one scale
+ * 2^e, -127 <= e <= 127; what is held is code * 2^e.  Codes (OCP e4m3 without
+ * infinities, or e5m2) lie in rows of `pitch` bytes; those behind the last
+ * column up to the end of its block must be 0, and every call here writes them
+ * so.  Scales are bytes e + 127, four blocks of a row together:
+ *   scale of (row, block) = scales[4 * ((block / 4) * scale_pitch + row) + block % 4]
+ * Bytes of blocks that a row does not have are neither read nor written. */
+typedef struct {
+    void* codes;          /* 16-byte aligned                                             */
+    void* scales;         /* 4-byte aligned; ceil(cols / 512) groups of scale_pitch words */
+    int64_t rows, cols;
+    int64_t pitch;        /* bytes: a multiple of 16, at least cols rounded up to 128     */
+    int64_t scale_pitch;  /* 4-byte words, at least rows                                  */
+    int32_t format;       /* shampoo_format8                                              */
+    int32_t reserved;     /* must be 0                                                    */
+} shampoo_matrix8;
+
+/* x (rows x cols, shampoo_dtype) in 8 bits: by its rows (`rows`: rows x cols),
+ * by its columns (`cols`: its transpose, cols x rows), or both with one reading;
+ * NULL leaves one out.  A block's scale is the least 2^e, e >= -127, with which
+ * its largest finite magnitude is at most the format's largest value (448,
+ * 57344); values are rounded to the nearest code, halves to the even one.  A
+ * value that is not finite becomes NaN (in e5m2 an infinity stays one) and does
+ * not touch its block's scale.  Errors: SHAMPOO_E_ARG (null or misaligned
+ * pointers, negative sizes, shapes that do not fit, unknown types, overlap),
+ * SHAMPOO_E_UNSUPPORTED (2^24 or more tiles of 128 x 128), SHAMPOO_E_HIP. */
+int shampoo_quantize8(const void* x, int32_t type, int64_t pitch, int64_t nrows, int64_t ncols,
+                      const shampoo_matrix8* rows, const shampoo_matrix8* cols, void* stream);
+/* The transpose of an 8-bit matrix, its values scaled anew along the other
+ * side: what dW needs of an activation that was kept in 8 bits.  A value is
+ * rounded again only where the new scale leaves it below the format's normal
+ * range (2^-14 of the block's largest for e4m3, 2^-29 for e5m2, or less).
+ * Errors: as above. */
+int shampoo_transpose8(const shampoo_matrix8* m, const shampoo_matrix8* out, void* stream);
+
+/* Root-mean-square norm of every row, with the residual's addition before it
+ * and an output in 8 bits:
+ *   z = x + residual, rounded to the residual's type and written to `total`
+ *   r = 1 / sqrt(mean(z^2) + eps),  h = (z r) w
+ * in fp32 (sums too).  Without a residual z is x and total is not written.
+ * total may be the residual or x itself (the same address, pitch and type).
+ * h goes to out8 (e4m3, blocks along the row), to `out`, or to both. */
+typedef struct {
+    int64_t rows, dim;             /* dim >= 1 */
+    const void* x;
+    const void* residual;          /* or NULL */
+    void* total;                   /* with a residual; in its type */
+    const void* weight;            /* dim elements */
+    float* rstd;                   /* rows: r, for the gradient; or NULL */
+    const shampoo_matrix8* out8;   /* rows x dim, or NULL */
+    void* out;                     /* or NULL */
+    int64_t x_pitch, residual_pitch, total_pitch, out_pitch;
+    int32_t x_type, residual_type, weight_type, out_type;   /* shampoo_dtype */
+    double eps;                    /* > 0 and finite */
+} shampoo_rms_norm_args;
+/* Errors: SHAMPOO_E_ARG, SHAMPOO_E_UNSUPPORTED (out8 in e5m2; 2^32 or more
+ * threads: 2^22 rows where dim > 8192, 2^24 at least otherwise),
+ * SHAMPOO_E_HIP. */
+int shampoo_rms_norm8(const shampoo_rms_norm_args* args, void* stream);
+
+/* Its gradient, for g = dL/dh (the 8-bit rounding counts as the identity):
+ *   a = w g,  dz = r (a - z r mean(a z r)) + add,  dw = sum over the rows of g z r
+ * in fp32.  add: the gradient that reaches z by its other uses (the residual
+ * stream).  z, add and dz have one type; dz, the gradient of x and of the
+ * residual, may be grad, z or add itself (the same address, pitch and type). */
+typedef struct {
+    int64_t rows, dim;             /* dim >= 1 */
+    const void* grad;
+    const void* z;                 /* the forward's total (or x)                     */
+    const float* rstd;             /* the forward's                                  */
+    const void* weight;
+    const void* add;               /* or NULL                                        */
+    void* dz;
+    float* dw;                     /* dim; or NULL                                   */
+    int64_t grad_pitch, z_pitch, add_pitch, dz_pitch;
+    int32_t grad_type, z_type, weight_type;
+    int32_t accumulate;            /* 1: dw is added to what is there                */
+} shampoo_rms_norm_grad_args;
+/* Bytes of workspace (16-byte aligned, the contents mean nothing before or
+ * after; one for each call that may run at the same time).  Host only. */
+int shampoo_rms_norm8_backward_workspace(int64_t rows, int64_t dim, size_t* bytes);
+/* Errors: SHAMPOO_E_ARG, SHAMPOO_E_STATE (workspace too small), SHAMPOO_E_HIP. */
+int shampoo_rms_norm8_backward(const shampoo_rms_norm_grad_args* args, void* workspace, size_t bytes,
+                               void* stream);
+
+/* c (a.rows x b.rows, shampoo_dtype) = A B^T, or c + A B^T (accumulate = 1), for
+ * 8-bit matrices with the same number of columns.  Sums are those of fp32
+ * where c is fp32; where it has 16 bits, eight products at a time are added with
+ * those below 2^-13 of the largest cut off, which leaves some 2e-5 of the
+ * result (a fiftieth of bf16's rounding).  fp32: a factor below 2^-126 may count
+ * as 0.  A sum that leaves the range of c's type becomes infinite.  workspace: as above, NULL
+ * where shampoo_matmul8_workspace says 0 bytes.  Errors: SHAMPOO_E_ARG,
+ * SHAMPOO_E_STATE (workspace too small), SHAMPOO_E_UNSUPPORTED (2^24 or more
+ * tiles), SHAMPOO_E_HIP. */
+int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+int shampoo_matmul8(const shampoo_matrix8* a, const shampoo_matrix8* b, void* c, int32_t type,
+                    int64_t pitch, int32_t accumulate, void* workspace, size_t bytes, void* stream);
+
+/* ---- 8-bit copies of many weights ----
+ * Each weight and its transpose in e4m3, one scale for each 128 x 128 values
+ * (the last ones of a side smaller), so that both hold the same values. */
+typedef struct shampoo_weights8_s shampoo_weights8_t; /* opaque; host memory only */
+
+typedef struct {
+    int64_t rows, cols;
+    int32_t type;      /* shampoo_dtype */
+    int32_t reserved;  /* must be 0 */
+} shampoo_weight_desc;
+
+/* Byte offsets in the state: the codes of each weight and then of its
+ * transpose, one after another, each from a multiple of 256 bytes on; then the
+ * scales in the same order.  What lies between them is 0. */
+typedef struct {
+    int64_t total;
+    int64_t off_codes, code_bytes;
+    int64_t off_scales, scale_bytes;
+} shampoo_weights8_layout;
+
+/* Plan for n weights.  Host only.  Errors: SHAMPOO_E_ARG (null, n < 1, negative
+ * sizes, unknown type, reserved not 0), SHAMPOO_E_UNSUPPORTED (2^24 or more
+ * tiles of 128 x 128, or a side of 2^31 or more), SHAMPOO_E_NOMEM. */
+int shampoo_weights8_create(int32_t n, const shampoo_weight_desc* weights, shampoo_weights8_t** out);
+int shampoo_weights8_get_layout(const shampoo_weights8_t* h, shampoo_weights8_layout* out);
+/* Attach the state (layout.total bytes, 256-byte aligned) and clear it; waits
+ * for that.  Errors: SHAMPOO_E_ARG, SHAMPOO_E_STATE (too small), SHAMPOO_E_HIP. */
+int shampoo_weights8_bind_state(shampoo_weights8_t* h, void* dev_state, size_t bytes, void* stream);
+/* The weights' device addresses (contiguous) from now on, until bound again.
+ * Errors: SHAMPOO_E_ARG (null, misaligned, or in the state), SHAMPOO_E_STATE,
+ * SHAMPOO_E_HIP. */
+int shampoo_weights8_bind_weights(shampoo_weights8_t* h, const void* const* weights, void* stream);
+/* All copies from the bound weights as they are now: one launch. */
+int shampoo_weights8_refresh(shampoo_weights8_t* h, void* stream);
+/* Copy i (transposed = 0) or its transpose (1), in the state.  Host only.
+ * Errors: SHAMPOO_E_ARG, SHAMPOO_E_STATE (no state bound). */
+int shampoo_weights8_matrix(const shampoo_weights8_t* h, int32_t i, int32_t transposed,
+                            shampoo_matrix8* out);
+void shampoo_weights8_destroy(shampoo_weights8_t* h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -201,12 +201,13 @@ class AdamW(_Bound):
         self._held = [self._held[0] if params is None else list(params),
                       self._held[1] if grads is None else list(grads)]
 
-    def step(self, lr, clip: Optional[GradNorm] = None):
+    def step(self, lr, clip: Optional[GradNorm] = None, copies8=None):
         """One step.  lr: a number, or one fp32 element on the device that the
         step reads when it runs.  clip: scale the gradients by the coefficient
         of its last compute, and skip the step where its norm is not finite.
         The gradients are those before clipping: not ones that clip_into has
-        scaled in place."""
+        scaled in place.  copies8: 8-bit copies of weights (fp8.Weights8) that
+        are refreshed behind it."""
         dev_lr = None
         if isinstance(lr, self.torch.Tensor):
             if lr.dtype != self.torch.float32 or lr.numel() != 1 or lr.device != self.device:
@@ -215,6 +216,8 @@ class AdamW(_Bound):
         if clip is not None and (clip.device != self.device or not clip.computed):
             raise ValueError(f"clip must be on {self.device} and have computed a norm")
         self._call(lib().shampoo_adamw_step, lr, dev_lr, None if clip is None else clip.record_ptr)
+        if copies8 is not None:
+            copies8.refresh()
 
     def set_step(self, t: int):
         """Set the number of steps done, the handle's and every tensor's own,

@@ -12,8 +12,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libshampoo_mi355x.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.cpp", "kernels.hip", "peaks.hip", "noalloc.hip",
-                                                     "adamw.cpp", "adamw.hip")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("common.hpp", "kernels.hpp", "adamw.hpp")] + [
+                                                     "adamw.cpp", "adamw.hip", "fp8.cpp", "fp8.hip",
+                                                     "fp8_matmul.hip")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("common.hpp", "kernels.hpp", "adamw.hpp", "fp8.hpp",
+                                                     "fp8_device.hpp")] + [
     os.path.join(ROOT, "include", "shampoo.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -97,6 +97,42 @@ class AdamWLayout(ctypes.Structure):
                  "off_m_scale", "off_s_scale", "runs_rem", "off_rem")]
 
 
+class Matrix8Desc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("pitch", ctypes.c_int64), ("scale_pitch", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64), ("dim", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("x", "residual", "total", "weight", "rstd",
+                                                  "out8", "out")]
+                + [(n, ctypes.c_int64) for n in ("x_pitch", "residual_pitch", "total_pitch",
+                                                 "out_pitch")]
+                + [(n, ctypes.c_int32) for n in ("x_type", "residual_type", "weight_type",
+                                                 "out_type")]
+                + [("eps", ctypes.c_double)])
+
+
+class RmsNormGradArgs(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64), ("dim", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("grad", "z", "rstd", "weight", "add", "dz", "dw")]
+                + [(n, ctypes.c_int64) for n in ("grad_pitch", "z_pitch", "add_pitch", "dz_pitch")]
+                + [(n, ctypes.c_int32) for n in ("grad_type", "z_type", "weight_type",
+                                                 "accumulate")])
+
+
+class WeightDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Weights8Layout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("total", "off_codes", "code_bytes", "off_scales", "scale_bytes")]
+
+
 # name -> (restype, argtypes); every symbol declared in include/shampoo.h
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -148,6 +184,26 @@ SIGNATURES = {
     "shampoo_adamw_set_tensor_steps": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int64), _P]),
     "shampoo_adamw_step": (ctypes.c_int, [_P, ctypes.c_double, _P, _P, _P]),
     "shampoo_adamw_destroy": (None, [_P]),
+    "shampoo_quantize8": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                         ctypes.c_int64, _P, _P, _P]),
+    "shampoo_transpose8": (ctypes.c_int, [_P, _P, _P]),
+    "shampoo_rms_norm8": (ctypes.c_int, [_P, _P]),
+    "shampoo_rms_norm8_backward_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+    "shampoo_rms_norm8_backward": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "shampoo_matmul8_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.POINTER(ctypes.c_size_t)]),
+    "shampoo_matmul8": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                       _P, ctypes.c_size_t, _P]),
+    "shampoo_weights8_create": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(WeightDesc),
+                                               ctypes.POINTER(_P)]),
+    "shampoo_weights8_get_layout": (ctypes.c_int, [_P, ctypes.POINTER(Weights8Layout)]),
+    "shampoo_weights8_bind_state": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
+    "shampoo_weights8_bind_weights": (ctypes.c_int, [_P, ctypes.POINTER(_P), _P]),
+    "shampoo_weights8_refresh": (ctypes.c_int, [_P, _P]),
+    "shampoo_weights8_matrix": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32,
+                                               ctypes.POINTER(Matrix8Desc)]),
+    "shampoo_weights8_destroy": (None, [_P]),
     "shampoo_destroy": (None, [_P]),
     "shampoo_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -356,9 +412,15 @@ class Shampoo(Plan):
         _check(lib().shampoo_precondition_and_apply(self.h, pa, ga, sp, self._stream()),
                "shampoo_precondition_and_apply")
 
-    def step(self, params, grads, step: int, cadence: int, sparse=None):
+    def step(self, params, grads, step: int, cadence: int, sparse=None, copies8=None):
         """One optimizer step (shampoo_step): statistics, roots when
-        step % cadence == 0, apply."""
+        step % cadence == 0, apply.  copies8: 8-bit copies of weights
+        (fp8.Weights8) that are refreshed behind it."""
+        self._step(params, grads, step, cadence, sparse)
+        if copies8 is not None:
+            copies8.refresh()
+
+    def _step(self, params, grads, step, cadence, sparse):
         pa, ga, sp, _keep = self._apply_args(params, grads, sparse)
         sel = root_selector(step, cadence, self.cfg.root_parts)
         if self.async_roots:
