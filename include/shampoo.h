@@ -626,7 +626,7 @@ typedef enum { SHAMPOO_E4M3 = 0, SHAMPOO_E5M2 = 1 } shampoo_format8;
  * column up to the end of its block must be 0, and every call here writes them
  * so.  Scales are bytes e + 127, four blocks of a row together:
  *   scale of (row, block) = scales[4 * ((block / 4) * scale_pitch + row) + block % 4]
- * Bytes of blocks that a row does not have are neither read nor written. */
+ * Bytes of blocks that a row does not have mean nothing and are not written. */
 typedef struct {
     void* codes;          /* 16-byte aligned                                             */
     void* scales;         /* 4-byte aligned; ceil(cols / 512) groups of scale_pitch words */
@@ -712,9 +712,9 @@ int shampoo_rms_norm8_backward(const shampoo_rms_norm_grad_args* args, void* wor
  * result (a fiftieth of bf16's rounding).  fp32: a factor below 2^-126 may count
  * as 0.  A sum that leaves the range of c's type becomes infinite.  workspace: as above, NULL
  * where shampoo_matmul8_workspace says 0 bytes.  Errors: SHAMPOO_E_ARG,
- * SHAMPOO_E_STATE (workspace too small), SHAMPOO_E_UNSUPPORTED (2^24 or more
- * tiles), SHAMPOO_E_HIP. */
-int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+ * SHAMPOO_E_STATE (workspace too small), SHAMPOO_E_UNSUPPORTED (2^22 or more
+ * tiles; rows more than 2^23 bytes apart), SHAMPOO_E_HIP. */
+int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, int32_t type, size_t* bytes);
 int shampoo_matmul8(const shampoo_matrix8* a, const shampoo_matrix8* b, void* c, int32_t type,
                     int64_t pitch, int32_t accumulate, void* workspace, size_t bytes, void* stream);
 

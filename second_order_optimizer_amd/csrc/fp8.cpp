@@ -81,6 +81,9 @@ bool matrix8(const shampoo_matrix8* m, int64_t rows, int64_t cols, Area& codes, 
            spans(codes) && spans(scales);
 }
 
+// Whether offsets inside 256 rows of it, and of its scales, fit 32 bits.
+bool rows_fit(const shampoo_matrix8* m) { return m->pitch <= (int64_t)1 << 23; }
+
 Mat8 device_view(const shampoo_matrix8* m) {
     return Mat8{reinterpret_cast<uint64_t>(m->codes), reinterpret_cast<uint64_t>(m->scales), m->pitch, m->scale_pitch};
 }
@@ -290,9 +293,9 @@ int shampoo_rms_norm8_backward(const shampoo_rms_norm_grad_args* a, void* worksp
     return status_of(launch_norm_bwd(a->grad_type, a->z_type, k, static_cast<hipStream_t>(stream)));
 }
 
-int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes) {
-    if (!bytes || !size_ok(m) || !size_ok(n) || !size_ok(k)) return SHAMPOO_E_ARG;
-    *bytes = mul8_workspace(plan_mul8(m, n, k), m, n);
+int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, int32_t type, size_t* bytes) {
+    if (!bytes || !size_ok(m) || !size_ok(n) || !size_ok(k) || !type_ok(type)) return SHAMPOO_E_ARG;
+    *bytes = mul8_workspace(plan_mul8(m, n, k, type), m, n);
     return SHAMPOO_OK;
 }
 
@@ -306,7 +309,8 @@ int shampoo_matmul8(const shampoo_matrix8* a, const shampoo_matrix8* b, void* c,
     if (!matrix8(a, m, k, in[0], in[1]) || !matrix8(b, n, k, in[2], in[3])) return SHAMPOO_E_ARG;
     if (!wide(c, type, pitch, m, n, out[0])) return SHAMPOO_E_ARG;
     if (out[0].empty()) return SHAMPOO_OK;
-    const Mul8Plan p = plan_mul8(m, n, k);
+    if (!rows_fit(a) || !rows_fit(b)) return SHAMPOO_E_UNSUPPORTED;
+    const Mul8Plan p = plan_mul8(m, n, k, type);
     if (!mul8_fits(p, m, n)) return SHAMPOO_E_UNSUPPORTED;
     const size_t need = mul8_workspace(p, m, n);
     if (need) {

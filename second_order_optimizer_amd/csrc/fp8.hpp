@@ -89,7 +89,7 @@ struct Mul8Plan {
     int32_t kind;
     int32_t splits, blocks_per_split;
 };
-Mul8Plan plan_mul8(int64_t m, int64_t n, int64_t k);
+Mul8Plan plan_mul8(int64_t m, int64_t n, int64_t k, int type);
 size_t mul8_workspace(const Mul8Plan& p, int64_t m, int64_t n);
 // Whether a launch takes that many tiles.
 bool mul8_fits(const Mul8Plan& p, int64_t m, int64_t n);

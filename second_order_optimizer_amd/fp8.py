@@ -153,7 +153,7 @@ def matmul(a: Matrix8, b: Matrix8, out, accumulate: bool = False):
     L = lib()
     _at8(b, b.rows, a.cols, dev, "b")
     at, code, pitch = _wide(out, (a.rows, b.rows), dev, "out")
-    need = _workspace(L.shampoo_matmul8_workspace, a.rows, b.rows, a.cols)
+    need = _workspace(L.shampoo_matmul8_workspace, a.rows, b.rows, a.cols, code)
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _run(dev, L.shampoo_matmul8, a.ptr, b.ptr, at, code, pitch, 1 if accumulate else 0,
          work.data_ptr() if need else None, need)

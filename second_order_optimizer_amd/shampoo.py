@@ -192,7 +192,7 @@ SIGNATURES = {
                                                             ctypes.POINTER(ctypes.c_size_t)]),
     "shampoo_rms_norm8_backward": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "shampoo_matmul8_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
-                                                 ctypes.POINTER(ctypes.c_size_t)]),
+                                                 ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
     "shampoo_matmul8": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                        _P, ctypes.c_size_t, _P]),
     "shampoo_weights8_create": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(WeightDesc),

@@ -88,10 +88,15 @@ def test_matmul_empty_and_nulls():
     assert matmul(b=m8(0, 300, D8, T8), c=None, pitch=0) == 0
     assert L.shampoo_matmul8(None, at(m8(1, 1)), OUT, 0, 1, 0, None, 0, None) == E_ARG
     n = ctypes.c_size_t()
-    assert L.shampoo_matmul8_workspace(1, 1, 1, None) == E_ARG
-    assert L.shampoo_matmul8_workspace(-1, 1, 1, ctypes.byref(n)) == E_ARG
+    assert L.shampoo_matmul8_workspace(1, 1, 1, 0, None) == E_ARG
+    assert L.shampoo_matmul8_workspace(-1, 1, 1, 0, ctypes.byref(n)) == E_ARG
     for m, k in ((0, 0), (1, 1), (7, 100000)):
-        assert L.shampoo_matmul8_workspace(m, 5, k, ctypes.byref(n)) == 0
+        assert L.shampoo_matmul8_workspace(m, 5, k, 0, ctypes.byref(n)) == 0
+    assert L.shampoo_matmul8_workspace(1, 1, 1, 3, ctypes.byref(n)) == E_ARG
+    # a long sum into a small matrix goes in parts, whose sums need memory
+    assert L.shampoo_matmul8_workspace(512, 512, 65536, 0, ctypes.byref(n)) == 0 and n.value % (512 * 512 * 4) == 0 and n.value
+    far = m8(3, 300, pitch=(1 << 23) + 128)
+    assert matmul(a=far) == E_UNSUPPORTED
 
 
 def norm(**kw):

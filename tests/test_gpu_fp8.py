@@ -438,7 +438,9 @@ def random8(rng, rows, cols, fmt, decades=0.5):
 
 PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 1000, 1000), (2, 300, 129), (15, 17, 640), (16, 256, 512), (17, 257, 300), (33, 64, 2000),
             (64, 4096, 130), (65, 1, 1025), (100, 3, 5000), (128, 128, 128), (129, 255, 384), (200, 777, 1030), (256, 256, 256),
-            (257, 513, 640), (300, 500, 0), (511, 1, 77), (600, 1300, 1500), (1, 5, 20000), (48, 96, 30000), (1024, 512, 8200)]
+            (257, 513, 640), (300, 500, 0), (511, 1, 77), (600, 1300, 1500), (1, 5, 20000), (48, 96, 30000), (1024, 512, 8200),
+            # every size of tile, whole and with ragged ends, and sums in parts
+            (2048, 2048, 256), (2049, 2100, 300), (4100, 4001, 129), (4096, 4096, 128), (4099, 4103, 1152), (2300, 4600, 1400), (513, 520, 33000)]
 
 
 @pytest.mark.parametrize("mnk", PRODUCTS)
