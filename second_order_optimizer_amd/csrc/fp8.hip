@@ -359,32 +359,40 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_norm_fwd(const NormFwd
 }
 
 // dz = r (a - x mean(a x)) + add with a = w g, x = z r, and this workgroup's
-// part of dw = sum over the rows of g x, which stays in registers over the
-// rows that it takes (V = 0: in its slot of the partial sums).
+// part of dw = sum over the rows of g x.  Memory bounds it.  Groups of W waves
+// take rows in turn; each thread's part of dw stays in registers over them, the
+// groups' are added up in LDS in their order, and what remains, a row for each
+// of at most 512 workgroups, is a sixteenth of what 8192 rows of 4096 read
+// (V = 0: dw grows in that row, in memory).
+constexpr int bwd_groups(int waves) { return waves < 8 ? 8 / waves : 1; }
+
 template <int GT, int ZT, int V, int W>
-__global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_norm_bwd(const NormBwdArgs a) {
-    constexpr int kGroups = W < 4 ? 4 / W : 1;
+__global__ __launch_bounds__(64 * W * bwd_groups(W)) void k_norm_bwd(const NormBwdArgs a) {
+    constexpr int kGroups = bwd_groups(W);
     __shared__ float s_sum[2][kGroups][16];
-    const int wave = threadIdx.x >> 6, lane = (wave % W) * 64 + (threadIdx.x & 63);
-    const int64_t slot = (int64_t)blockIdx.x * kGroups + wave / W;
-    const int64_t turns = (a.rows + a.slots - 1) / a.slots;
+    __shared__ float s_dw[V > 0 && kGroups > 1 ? V * W * 512 : 1];
+    const int wave = threadIdx.x >> 6, lane = (wave % W) * 64 + (threadIdx.x & 63), mine = wave / W;
+    const int64_t group = (int64_t)blockIdx.x * kGroups + mine, groups = (int64_t)a.slots * kGroups;
+    const int64_t turns = (a.rows + groups - 1) / groups;
+    const uint64_t partial = reinterpret_cast<uint64_t>(a.partials) + (uint64_t)blockIdx.x * (uint64_t)a.dim * 4;
+    const float inv_dim = 1.f / (float)a.dim;
     float dw[V > 0 ? V : 1][8] = {};
     int phase = 0;
     for (int64_t t = 0; t < turns; ++t, phase ^= 1) {
-        const int64_t want = t * a.slots + slot;
+        const int64_t want = t * groups + group;
         const bool live = want < a.rows;
         const int64_t row = live ? want : a.rows - 1;
         const int64_t gat = row * a.g.pitch, zat = row * a.z.pitch, aat = row * a.add.pitch, dat = row * a.dz.pitch;
         const float r = live ? a.rstd[row] : 0.f;   // a row that is not there adds 0 to dw
-        const float inv_dim = 1.f / (float)a.dim;
         float dot = 0.f;
         if constexpr (V > 0) {
-            float g[V][8], x[V][8];
+            float g[V][8], x[V][8], add[V][8] = {};
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int64_t c = (int64_t)(v * W * 64 + lane) * 8, left = live ? a.dim - c : 0;
                 widen8<GT>(load8_upto<GT>(a.g.ptr, gat + c, left), g[v]);
                 widen8<ZT>(load8_upto<ZT>(a.z.ptr, zat + c, left), x[v]);
+                if (a.add.ptr) widen8<ZT>(load8_upto<ZT>(a.add.ptr, aat + c, left), add[v]);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -403,12 +411,10 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_norm_bwd(const NormBwd
             if (live) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const int64_t c = (int64_t)(v * W * 64 + lane) * 8, left = a.dim - c;
-                    float add[8] = {};
-                    if (a.add.ptr) widen8<ZT>(load8_upto<ZT>(a.add.ptr, aat + c, left), add);
+                    const int64_t c = (int64_t)(v * W * 64 + lane) * 8;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) add[k] += r * (g[v][k] - x[v][k] * dot);
-                    store8_upto<ZT>(a.dz.ptr, dat + c, left, add);
+                    for (int k = 0; k < 8; ++k) add[v][k] += r * (g[v][k] - x[v][k] * dot);
+                    store8_upto<ZT>(a.dz.ptr, dat + c, a.dim - c, add[v]);
                 }
             }
         } else {
@@ -419,15 +425,14 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_norm_bwd(const NormBwd
                 widen8<ZT>(load8_upto<ZT>(a.z.ptr, zat + c, left), x);
                 weight8(a.w, a.w_type, c, a.dim - c, w);
                 float part[8] = {};
-                const uint64_t p = reinterpret_cast<uint64_t>(a.partials);
-                if (t && a.dw) widen8<DT_F32>(load8_upto<DT_F32>(p, slot * a.dim + c, a.dim - c), part);
+                if (t && a.dw) widen8<DT_F32>(load8_upto<DT_F32>(partial, c, a.dim - c), part);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     x[k] *= r;
                     part[k] = fmaf(g[k], x[k], part[k]);
                     dot = fmaf(g[k] * w[k], x[k], dot);
                 }
-                if (a.dw) store8_upto<DT_F32>(p, slot * a.dim + c, a.dim - c, part);
+                if (a.dw) store8_upto<DT_F32>(partial, c, a.dim - c, part);
             }
             dot = row_sum<W>(dot, s_sum[phase], wave) * inv_dim;
             if (live) {
@@ -447,10 +452,23 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_norm_bwd(const NormBwd
     }
     if constexpr (V > 0) {
         if (a.dw) {
+            for (int q = 0; q < kGroups; ++q) {
+                if (mine == q) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int64_t c = (int64_t)(v * W * 64 + lane) * 8;
-                store8_upto<DT_F32>(reinterpret_cast<uint64_t>(a.partials), slot * a.dim + c, a.dim - c, dw[v]);
+                    for (int v = 0; v < V; ++v) {
+                        const int c = (v * W * 64 + lane) * 8;
+                        if constexpr (kGroups > 1) {
+                            float* p = s_dw + c;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                if (q) dw[v][k] += p[k];
+                                if (q + 1 < kGroups) p[k] = dw[v][k];
+                            }
+                        }
+                        if (q + 1 == kGroups) store8_upto<DT_F32>(partial, c, a.dim - c, dw[v]);
+                    }
+                }
+                if constexpr (kGroups > 1) __syncthreads();
             }
         }
     }
@@ -462,13 +480,24 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const NormBwdArgs a) {
     __shared__ float s[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
-    const int per = (a.slots + 31) / 32;
+    const int per = (a.slots + 31) / 32, from = y * per, to = from + per < a.slots ? from + per : a.slots;
     float sum = 0.f;
-    if (c < a.dim)
-        for (int i = y * per; i < (y + 1) * per && i < a.slots; ++i) sum += a.partials[(int64_t)i * a.dim + c];
+    if (c < a.dim) {
+        const float* p = a.partials + c;
+        int i = from;
+        for (; i + 8 <= to; i += 8) {       // eight loads on their way together
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(i + k) * a.dim];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k];
+        }
+        for (; i < to; ++i) sum += p[(int64_t)i * a.dim];
+    }
     s[y][x] = sum;
     __syncthreads();
     if (y == 0 && c < a.dim) {
+#pragma unroll
         for (int k = 1; k < 32; ++k) sum += s[k][x];
         a.dw[c] = a.accumulate ? a.dw[c] + sum : sum;
     }
@@ -574,8 +603,8 @@ void norm_fwd(int rt, const NormFwdArgs& a, hipStream_t s) {
 template <int GT, int ZT>
 void norm_bwd(const NormBwdArgs& a, hipStream_t s) {
     const RowShape sh = row_shape(a.dim);
-    const dim3 grid(a.slots / groups_of(sh));
-#define N(V, W) k_norm_bwd<GT, ZT, V, W><<<grid, W < 4 ? 256 : 64 * W, 0, s>>>(a)
+    const dim3 grid(a.slots);
+#define N(V, W) k_norm_bwd<GT, ZT, V, W><<<grid, 64 * W * bwd_groups(W), 0, s>>>(a)
     if (sh.chunks == 0) N(0, 16);
     else if (sh.waves == 1 && sh.chunks == 1) N(1, 1);
     else if (sh.waves == 1) N(2, 1);
@@ -607,12 +636,11 @@ hipError_t launch_norm_fwd(int xt, int rt, const NormFwdArgs& a, hipStream_t s) 
     return hipGetLastError();
 }
 
+// Workgroups of the gradient, each of which leaves a row of partial sums.
 int norm_bwd_slots(int64_t rows, int64_t dim) {
-    const RowShape sh = row_shape(dim);
-    const int g = groups_of(sh);
-    const int64_t most = sh.waves <= 4 ? 1024 : sh.waves == 8 ? 512 : 256;
-    const int64_t want = rows < most * g ? rows : most * g;
-    return (int)((want + g - 1) / g * g);
+    const int g = bwd_groups(row_shape(dim).waves);
+    const int64_t want = (rows + g - 1) / g;
+    return (int)(want < 512 ? want : 512);
 }
 
 hipError_t launch_norm_bwd(int gt, int zt, const NormBwdArgs& a, hipStream_t s) {

@@ -28,6 +28,8 @@ library has not been built -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -40,16 +42,17 @@ FORMATS = {"e4m3": 0, "e5m2": 1}
 BLOCK = 128
 _CODES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32 = (torch.float32,)
 
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                   lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current = torch.cuda.current_device
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(device, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
     index = device.index
-    if device.type != "cuda":
+    if index is None or device.type != "cuda":
         raise ValueError(f"no kernels for {device}")
     if _current() == index:
         rc = fn(*args, _stream(index))
@@ -60,17 +63,21 @@ def _run(device, fn, *args):
         _check(rc, fn.__name__)
 
 
-def _wide(t, shape, device, what):
+def _wide(t, rows, cols, device, what):
     """(address, type, pitch) of a wide matrix."""
     code = _TYPES.get(t.dtype)
-    if code is None or t.dim() != 2 or t.device != device or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must be a 2-D fp32, bf16 or fp16 tensor"
-                         + (f" of {tuple(shape)}" if shape is not None else "") + f" on {device}")
-    rows, cols = t.shape
+    if code is None or t.shape != (rows, cols) or t.device != device:
+        raise ValueError(f"{what} must be an fp32, bf16 or fp16 tensor of {rows} x {cols} on {device}")
     pitch, step = t.stride()
-    if (step != 1 and cols > 1) or (pitch < cols and rows > 1):
+    if step != 1 and cols > 1 or pitch < cols and rows > 1:
         raise ValueError(f"{what}: the elements of a row must be neighbours and rows apart, got strides {t.stride()}")
-    return t.data_ptr(), code, max(pitch, cols)
+    return t.data_ptr(), code, pitch if pitch > cols else cols
+
+
+def _shape(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D, got {tuple(t.shape)}")
+    return t.shape
 
 
 def _vector(t, numel, device, what, types=_TYPES):
@@ -124,7 +131,7 @@ class Matrix8:
 
 
 def _at8(m, rows, cols, device, what):
-    if not isinstance(m, Matrix8) or m.rows != rows or m.cols != cols or m.device != device:
+    if type(m) is not Matrix8 or m.rows != rows or m.cols != cols or m.device != device:
         raise ValueError(f"{what} must be a Matrix8 of {rows} x {cols} on {device}")
     return m.ptr
 
@@ -133,8 +140,8 @@ def quantize(x, rows: Optional[Matrix8] = None, cols: Optional[Matrix8] = None):
     """x in 8 bits: by its rows into ``rows`` (x's shape), by its columns into
     ``cols`` (its transpose's shape), or both with one reading of x."""
     dev = x.device
-    at, code, pitch = _wide(x, None, dev, "x")
-    r, c = x.shape
+    r, c = _shape(x, "x")
+    at, code, pitch = _wide(x, r, c, dev, "x")
     if rows is None and cols is None:
         raise ValueError("quantize: neither rows nor cols")
     _run(dev, lib().shampoo_quantize8, at, code, pitch, r, c,
@@ -152,8 +159,8 @@ def matmul(a: Matrix8, b: Matrix8, out, accumulate: bool = False):
     dev = a.device
     L = lib()
     _at8(b, b.rows, a.cols, dev, "b")
-    at, code, pitch = _wide(out, (a.rows, b.rows), dev, "out")
-    need = _workspace(L.shampoo_matmul8_workspace, a.rows, b.rows, a.cols, code)
+    at, code, pitch = _wide(out, a.rows, b.rows, dev, "out")
+    need = _matmul_workspace(a.rows, b.rows, a.cols, code)
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _run(dev, L.shampoo_matmul8, a.ptr, b.ptr, at, code, pitch, 1 if accumulate else 0,
          work.data_ptr() if need else None, need)
@@ -168,6 +175,24 @@ def _workspace(fn, *sizes):
     return out.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(m, n, k, code):     # by the sizes alone
+    return _workspace(lib().shampoo_matmul8_workspace, m, n, k, code)
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace(rows, dim):
+    return _workspace(lib().shampoo_rms_norm8_backward_workspace, rows, dim)
+
+
+# RmsNormArgs and RmsNormGradArgs as bytes: a third of the time that a ctypes
+# structure of twenty fields takes
+_pack_norm = struct.Struct("=2q7Q4q4id").pack
+_pack_norm_grad = struct.Struct("=2q7Q4q4i").pack
+assert struct.calcsize("=2q7Q4q4id") == ctypes.sizeof(RmsNormArgs)
+assert struct.calcsize("=2q7Q4q4i") == ctypes.sizeof(RmsNormGradArgs)
+
+
 def rms_norm(x, weight, eps: float, *, residual=None, total=None, out8: Optional[Matrix8] = None,
              out=None, rstd=None):
     """z = x + residual (into ``total``, in the residual's type; without a
@@ -175,24 +200,23 @@ def rms_norm(x, weight, eps: float, *, residual=None, total=None, out8: Optional
     ``rstd``), h = (z r) weight into ``out8`` (e4m3), ``out``, or both.
     total may be the residual or x itself."""
     dev = x.device
-    xp, xt, xs = _wide(x, None, dev, "x")
-    shape = x.shape
-    rows, dim = shape
+    rows, dim = _shape(x, "x")
+    xp, xt, xs = _wide(x, rows, dim, dev, "x")
     rp = rt = rs = tp = ts = op = ot = os = 0
-    if (residual is None) != (total is None):
-        raise ValueError("a residual and total are given together")
-    if residual is not None:
-        rp, rt, rs = _wide(residual, shape, dev, "residual")
-        tp, tt, ts = _wide(total, shape, dev, "total")
+    if residual is not None and total is not None:
+        rp, rt, rs = _wide(residual, rows, dim, dev, "residual")
+        tp, tt, ts = _wide(total, rows, dim, dev, "total")
         if tt != rt:
             raise ValueError(f"total has the residual's type, {residual.dtype}")
+    elif residual is not None or total is not None:
+        raise ValueError("a residual and total are given together")
     if out is not None:
-        op, ot, os = _wide(out, shape, dev, "out")
-    a = RmsNormArgs(rows, dim, xp, rp, tp, _vector(weight, dim, dev, "weight"),
-                    None if rstd is None else _vector(rstd, rows, dev, "rstd", (torch.float32,)),
-                    None if out8 is None else _at8(out8, rows, dim, dev, "out8"), op,
-                    xs, rs, ts, os, xt, rt, _TYPES[weight.dtype], ot, eps)
-    _run(dev, lib().shampoo_rms_norm8, ctypes.addressof(a))
+        op, ot, os = _wide(out, rows, dim, dev, "out")
+    a = _pack_norm(rows, dim, xp, rp, tp, _vector(weight, dim, dev, "weight"),
+                   0 if rstd is None else _vector(rstd, rows, dev, "rstd", _F32),
+                   0 if out8 is None else _at8(out8, rows, dim, dev, "out8"), op,
+                   xs, rs, ts, os, xt, rt, _TYPES[weight.dtype], ot, eps)
+    _run(dev, lib().shampoo_rms_norm8, a)
 
 
 def rms_norm_backward(grad, z, rstd, weight, *, dz, add=None, dw=None, accumulate: bool = False):
@@ -202,27 +226,24 @@ def rms_norm_backward(grad, z, rstd, weight, *, dz, add=None, dw=None, accumulat
     the weight, or added to what is there.  dz has z's type and may be add,
     grad or z itself."""
     dev = z.device
-    gp, gt, gs = _wide(grad, z.shape, dev, "grad")
-    zp, zt, zs = _wide(z, None, dev, "z")
-    dp, dt, ds = _wide(dz, z.shape, dev, "dz")
+    rows, dim = _shape(z, "z")
+    gp, gt, gs = _wide(grad, rows, dim, dev, "grad")
+    zp, zt, zs = _wide(z, rows, dim, dev, "z")
+    dp, dt, ds = _wide(dz, rows, dim, dev, "dz")
     ap = at = as_ = 0
     if add is not None:
-        ap, at, as_ = _wide(add, z.shape, dev, "add")
+        ap, at, as_ = _wide(add, rows, dim, dev, "add")
     if dt != zt or (add is not None and at != zt):
         raise ValueError(f"dz and add have z's type, {z.dtype}")
-    rows, dim = z.shape
-    L = lib()
-    need = 0
-    work = None
-    f32 = (torch.float32,)
+    wp = need = work = 0
     if dw is not None:
-        need = _workspace(L.shampoo_rms_norm8_backward_workspace, rows, dim)
+        wp = _vector(dw, dim, dev, "dw", _F32)
+        need = _norm_workspace(rows, dim)
         work = torch.empty(need, dtype=torch.uint8, device=dev)
-    a = RmsNormGradArgs(rows, dim, gp, zp, _vector(rstd, rows, dev, "rstd", f32),
-                        _vector(weight, dim, dev, "weight"), ap, dp,
-                        None if dw is None else _vector(dw, dim, dev, "dw", f32),
+    a = _pack_norm_grad(rows, dim, gp, zp, _vector(rstd, rows, dev, "rstd", _F32),
+                        _vector(weight, dim, dev, "weight"), ap, dp, wp,
                         gs, zs, as_, ds, gt, zt, _TYPES[weight.dtype], 1 if accumulate else 0)
-    _run(dev, L.shampoo_rms_norm8_backward, ctypes.addressof(a), work.data_ptr() if need else None, need)
+    _run(dev, lib().shampoo_rms_norm8_backward, a, work.data_ptr() if need else None, need)
 
 
 class Weights8(_Bound):
