@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fp8.hpp"
 #include "fp8_device.hpp"
@@ -91,12 +92,31 @@ __device__ __forceinline__ void quantize_tile(const QuantJob& j, int64_t tr, int
 #pragma unroll
             for (int i = 0; i < 8; ++i) raw[i] = load8<SRC>(j.x.ptr, (r0 + i) * j.x.pitch + c0);
         } else {
+            // one branch around all the loads of a kind, so that they are on
+            // their way together; rows behind the last are that one, for nothing
+            const int64_t left = j.ncols - c0;
+            const auto at = [&](int i) { return (r0 + i < j.nrows ? r0 + i : j.nrows - 1) * j.x.pitch + c0; };
+            if (left >= 8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                raw[i] = load8_upto<SRC>(j.x.ptr, (r0 + i) * j.x.pitch + c0, r0 + i < j.nrows ? j.ncols - c0 : 0);
+                for (int i = 0; i < 8; ++i) raw[i] = load8<SRC>(j.x.ptr, at(i));
+            } else if (left > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) raw[i] = load8_part<SRC>(j.x.ptr, at(i), left);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) raw[i] = Raw8<SRC>{};
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) widen8<SRC>(raw[i], v[i]);
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r0 + i >= j.nrows) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+                }
+        }
     } else {
         // rows of an 8-bit matrix are whole blocks
         u32x2 raw[8];
@@ -124,20 +144,28 @@ __device__ __forceinline__ void quantize_tile(const QuantJob& j, int64_t tr, int
         }
     }
 
+    // Largest magnitudes as bits, in which whatever is not finite is larger than
+    // all that is: only where one turns up are they taken again without it.
     uint32_t rmax[8], cmax[8];
+    const auto largest = [&](auto finite) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        rmax[k] = 0;
-        cmax[k] = 0;
+        for (int k = 0; k < 8; ++k) rmax[k] = cmax[k] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t u = decltype(finite)::value ? finite_bits(v[i][k]) : __float_as_uint(v[i][k]) & 0x7FFFFFFFu;
+                if (ROWS || SHARED) rmax[i] = umax(rmax[i], u);
+                if (COLS && !SHARED) cmax[k] = umax(cmax[k], u);
+            }
+    };
+    largest(std::integral_constant<bool, false>());
+    {
+        uint32_t all = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = umax(all, ROWS || SHARED ? rmax[i] : cmax[i]);
+        if (__any(all >= 0x7F800000u)) largest(std::integral_constant<bool, true>());
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t u = finite_bits(v[i][k]);
-            if (ROWS || SHARED) rmax[i] = umax(rmax[i], u);
-            if (COLS && !SHARED) cmax[k] = umax(cmax[k], u);
-        }
     if constexpr (SHARED) {
         uint32_t all = rmax[0];
 #pragma unroll

@@ -55,27 +55,34 @@ __device__ __forceinline__ Raw8<DT> load8(uint64_t base, int64_t at) {
     }
     return r;
 }
-// The first `left` of them (none where it is not positive), 0 for the others.
+// The first `left` of them, 1 to 7, and 0 for the others; without a branch, so
+// that the eight loads are on their way together.
 template <int DT>
-__device__ __forceinline__ Raw8<DT> load8_upto(uint64_t base, int64_t at, int64_t left) {
+__device__ __forceinline__ Raw8<DT> load8_part(uint64_t base, int64_t at, int64_t left) {
     typedef typename Elem<DT>::type T;
-    if (left >= 8) return load8<DT>(base, at);
     const T* p = gptr<const T>(base) + at;
+    const int n = (int)left;
+    T e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = p[k < n ? k : n - 1];
     Raw8<DT> r;
-    if constexpr (DT == DT_F32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            r.lo[k] = k < left ? p[k] : 0.f;
-            r.hi[k] = k + 4 < left ? p[k + 4] : 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t a = 2 * k < left ? p[2 * k] : 0u, b = 2 * k + 1 < left ? p[2 * k + 1] : 0u;
-            r.w[k] = a | b << 16;
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == DT_F32) {
+            r.lo[k] = k < n ? e[k] : 0.f;
+            r.hi[k] = k + 4 < n ? e[k + 4] : 0.f;
+        } else {
+            r.w[k] = (2 * k < n ? (uint32_t)e[2 * k] : 0u) | (2 * k + 1 < n ? (uint32_t)e[2 * k + 1] : 0u) << 16;
         }
     }
     return r;
+}
+// As many of them as there are, none where `left` is not positive.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8_upto(uint64_t base, int64_t at, int64_t left) {
+    if (left >= 8) return load8<DT>(base, at);
+    if (left > 0) return load8_part<DT>(base, at, left);
+    return Raw8<DT>{};
 }
 
 __device__ __forceinline__ float half_value(uint32_t u) {
