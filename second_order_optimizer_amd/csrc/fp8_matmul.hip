@@ -646,6 +646,102 @@ __global__ __launch_bounds__(256) void k_mul8_big(const Mul8Args a, const uint32
     });
 }
 
+// Tiles of 64 x 64 by eight waves, for products of few tiles, where the time is
+// that of one block after another: two waves share 32 x 32 of C, each taking one
+// half of every block, and join their sums in LDS; four stages, three of them on
+// their way.  777 x 1000 x 2048: 9.9 us in fp32, 7.3 in bf16, against 11.3 and 7.6
+// where one wave took both halves; eight stages, or two blocks between barriers,
+// made no difference.
+template <int FA, int FB, bool EXACT>
+__global__ __launch_bounds__(512) void k_mul8_small(const Mul8Args a, const uint32_t tiles_m, const uint32_t tiles_n) {
+    constexpr int BM = 64, BN = 64, STAGES = 4;
+    constexpr uint32_t kStage = (BM + BN) * kBlock8, kWords = STAGES * kStage;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1 & 1, mine = wave >> 2;      // mine: the half of a block
+    const Tile t = tile_of(blockIdx.x, gridDim.x, tiles_m, tiles_n);
+    const int64_t m0 = t.m * BM, n0 = t.n * BN;
+    const int64_t all = (a.k + kBlock8 - 1) / kBlock8;
+    const int64_t kb0 = (int64_t)t.split * a.blocks_per_split;
+    const int nkb = (int)(all - kb0 < a.blocks_per_split ? all - kb0 : a.blocks_per_split);
+
+    // each wave loads eight rows of A and eight of B
+    const int lr = wave * 8 + (lane >> 3);
+    const uint32_t lc = 16 * ((lane & 7) ^ (lr >> 1 & 7));
+    const uint32_t offa = (uint32_t)((m0 + lr < a.m ? lr : a.m - 1 - m0) * a.a.pitch) + lc;
+    const uint32_t offb = (uint32_t)((n0 + lr < a.n ? lr : a.n - 1 - n0) * a.b.pitch) + lc;
+    uint64_t basea = a.a.codes + (uint64_t)(m0 * a.a.pitch + kb0 * kBlock8), baseb = a.b.codes + (uint64_t)(n0 * a.b.pitch + kb0 * kBlock8);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    const auto load = [&](int stage, int kb) {     // block kb, or the last one again
+        dma16(lds0 + stage * kStage + wave * 1024, basea, offa);
+        dma16(lds0 + stage * kStage + BM * kBlock8 + wave * 1024, baseb, offb);
+        const uint32_t step = kb + 1 < nkb ? kBlock8 : 0;
+        basea += step;
+        baseb += step;
+    };
+    // scale words: the even waves those of A's rows, the odd ones of B's
+    const int of_b = wave & 1;
+    const int64_t wfirst = of_b ? n0 : m0, wlast = (of_b ? a.n : a.m) - 1, wpitch = 4 * (of_b ? a.b.spitch : a.a.spitch);
+    uint64_t wbase = (of_b ? a.b.scales : a.a.scales) + 4 * (uint64_t)wfirst + (uint64_t)(kb0 / 4 * wpitch);
+    const uint32_t woff = 4 * (uint32_t)((wfirst + lane < wlast ? wfirst + lane : wlast) - wfirst);
+    const auto words = [&](int group, bool on) {
+        dma4(lds0 + kWords + ((group & 1) * (BM + BN) + of_b * 64) * 4, wbase, woff);
+        wbase += wpitch & -(int64_t)(on & (4 * (group + 1) < nkb));
+    };
+
+    const int row = lane & 31, half = lane >> 5;
+    const uint32_t chunk = 16 * ((2 * mine + half) ^ (row >> 1 & 7));
+    const uint32_t ra = (wm * 32 + row) * kBlock8 + chunk, rb = (BM + wn * 32 + row) * kBlock8 + chunk;
+    const auto operand_at = [&](uint32_t at) {
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + at), hi = *reinterpret_cast<const i32x4*>(lds + (at ^ 64));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    f32x16 acc;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+
+    if (nkb > 0) {
+        words(0, true);
+        for (int s = 0; s < STAGES - 1; ++s) load(s, s);
+        for (int kb = 0; kb < nkb; ++kb) {
+            const int stage = kb % STAGES;
+            // this block has arrived, the one before it has been read
+            stage_ready<2 * (STAGES - 2)>();
+            words((kb >> 2) + 1, (kb & 3) == 3);
+            load((kb + STAGES - 1) % STAGES, kb + STAGES - 1);
+            const unsigned char* w = reinterpret_cast<const unsigned char*>(lds) + kWords + (kb >> 2 & 1) * (BM + BN) * 4 + (kb & 3);
+            const int ex = w[4 * (wm * 32 + row)], ey = w[4 * (BM + wn * 32 + row)];
+            const i32x8 x = operand_at(stage * kStage + ra), y = operand_at(stage * kStage + rb);
+            if constexpr (EXACT) {
+                const float fx = __int_as_float(ex << 23), fy = __int_as_float(ey << 23);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widened<FB>(y[2 * u], y[2 * u + 1], fy), widened<FA>(x[2 * u], x[2 * u + 1], fx), acc, 0, 0, 0);
+            } else {
+                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc, FB, FA, 0, ey, 0, ex);
+            }
+        }
+        stage_ready<0>();    // no load is left, to these waves or to a workgroup that comes after
+    }
+
+    // the second halves' sums, then C by the waves of the first
+    f32x4* joined = reinterpret_cast<f32x4*>(lds + 2 * kStage) + (wave & 3) * 256 + lane;
+    if (mine) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) joined[q * 64] = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    }
+    __syncthreads();
+    if (mine) return;
+    constexpr int kPiece = 32 * 36;
+    static_assert(4 * kPiece * 4 <= (int)(2 * kStage), "a piece of LDS for each wave in front of the sums");
+    float* piece = reinterpret_cast<float*>(lds) + wave * kPiece;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(piece + row * 36 + 8 * q + 4 * half) = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]} + joined[q * 64];
+    __builtin_amdgcn_wave_barrier();
+    store_rows<EXACT, 32, 32>(a, t.split, piece, m0 + wm * 32, n0 + wn * 32);
+}
+
 // C from the parts' sums, in the order of the parts.
 __global__ __launch_bounds__(256) void k_mul8_join(const Mul8Args a) {
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, per = (a.n + 3) / 4 * 4;
@@ -685,6 +781,17 @@ hipError_t launch_big(const Mul8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int FA, int FB, bool EXACT>
+hipError_t launch_small(const Mul8Args& a, hipStream_t s) {
+    const uint32_t tm = (uint32_t)((a.m + 63) / 64), tn = (uint32_t)((a.n + 63) / 64);
+    constexpr int bytes = 4 * 128 * kBlock8 + 2 * 128 * 4;
+    const auto k = k_mul8_small<FA, FB, EXACT>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    k<<<tm * tn * a.splits, 512, bytes, s>>>(a, tm, tn);
+    return hipGetLastError();
+}
+
 template <int MT, int FA, int FB, bool EXACT>
 hipError_t launch_few(const Mul8Args& a, hipStream_t s) {
     const uint32_t grid = (uint32_t)((a.n + 15) / 16);
@@ -702,7 +809,7 @@ hipError_t launch_kind(int kind, const Mul8Args& a, hipStream_t s) {
         if (a.m <= 16) return launch_few<1, FA, FB, EXACT>(a, s);
         if (a.m <= 32) return launch_few<2, FA, FB, EXACT>(a, s);
         return launch_few<4, FA, FB, EXACT>(a, s);
-    case MUL8_64: return launch_tile<64, 64, 2, 2, 4, FA, FB, EXACT>(a, s);
+    case MUL8_64: return launch_small<FA, FB, EXACT>(a, s);
     case MUL8_128: return launch_tile<128, 128, 2, 2, 2, FA, FB, EXACT>(a, s);
     default:
         if constexpr (EXACT) return launch_tile<256, 256, 2, 4, 2, FA, FB, EXACT>(a, s);
