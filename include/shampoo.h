@@ -658,8 +658,8 @@ int shampoo_transpose8(const shampoo_matrix8* m, const shampoo_matrix8* out, voi
 /* Root-mean-square norm of every row, with the residual's addition before it
  * and an output in 8 bits:
  *   z = x + residual, rounded to the residual's type and written to `total`
- *   r = 1 / sqrt(mean(z^2) + eps),  h = (z r) w
- * in fp32 (sums too).  Without a residual z is x and total is not written.
+ *   r = 1 / sqrt(mean(z^2) + eps),  h = z r w
+ * in 64 bits, h and r rounded to fp32 and h then to its outputs.  Without a residual z is x and total is not written.
  * total may be the residual or x itself (the same address, pitch and type).
  * h goes to out8 (e4m3, blocks along the row), to `out`, or to both. */
 typedef struct {
@@ -673,7 +673,7 @@ typedef struct {
     void* out;                     /* or NULL */
     int64_t x_pitch, residual_pitch, total_pitch, out_pitch;
     int32_t x_type, residual_type, weight_type, out_type;   /* shampoo_dtype */
-    double eps;                    /* > 0 and finite */
+    double eps;                    /* 2^-120 to 2^120 */
 } shampoo_rms_norm_args;
 /* Errors: SHAMPOO_E_ARG, SHAMPOO_E_UNSUPPORTED (out8 in e5m2; 2^32 or more
  * threads: 2^22 rows where dim > 8192, 2^24 at least otherwise),

@@ -181,7 +181,7 @@ int shampoo_transpose8(const shampoo_matrix8* m, const shampoo_matrix8* out, voi
 
 int shampoo_rms_norm8(const shampoo_rms_norm_args* a, void* stream) {
     if (!a || !size_ok(a->rows) || !size_ok(a->dim) || a->dim < 1) return SHAMPOO_E_ARG;
-    if (!(a->eps > 0.0 && std::isfinite(a->eps) && (float)a->eps > 0.f && std::isfinite((float)a->eps))) return SHAMPOO_E_ARG;
+    if (!(a->eps > 0.0 && std::isfinite(a->eps)&& a->eps >= 0x1p-120 && a->eps <= 0x1p120)) return SHAMPOO_E_ARG;
     if ((a->residual != nullptr) != (a->total != nullptr) && a->rows) return SHAMPOO_E_ARG;
     const bool res = a->residual && a->total;
     Area in[3], out[5];
@@ -232,7 +232,7 @@ int shampoo_rms_norm8(const shampoo_rms_norm_args* a, void* stream) {
     k.rstd = a->rstd;
     k.rows = a->rows;
     k.dim = a->dim;
-    k.eps = (float)a->eps;
+    k.eps = a->eps;
     k.w_type = a->weight_type;
     k.out_type = a->out_type;
     return status_of(launch_norm_fwd(a->x_type, res ? a->residual_type : -1, k, static_cast<hipStream_t>(stream)));

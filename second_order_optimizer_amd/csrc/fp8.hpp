@@ -51,7 +51,7 @@ struct NormFwdArgs {
     const void* w;
     float* rstd;
     int64_t rows, dim;
-    float eps;
+    double eps;
     int32_t w_type, out_type;
 };
 

@@ -336,7 +336,7 @@ def test_norm_of_odd_rows():
     x[1] = 0
     x[2, 7] = np.nan
     x[3, 299] = np.inf
-    x[4] = 3e38          # the squares' sum leaves fp32: r = 0
+    x[4] = 3e38          # the squares' sum leaves fp32, not 64 bits
     x[5] = 1e-30         # eps is all that is left
     t, _ = wide(x, "f32")
     w = torch.ones(300, device="cuda")
@@ -344,8 +344,9 @@ def test_norm_of_odd_rows():
     F.rms_norm(t, w, 1e-6, out8=h8.m, rstd=r)
     v = h8.values()
     rr = np64(r)
-    assert np.all(v[1] == 0) and np.all(np.isnan(v[2])) and np.isnan(rr[2]) and rr[3] == 0 and rr[4] == 0
-    assert np.isnan(v[3, 299]) and np.all(v[3, :299] == 0) and np.all(v[4] == 0)
+    assert np.all(v[1] == 0) and np.all(np.isnan(v[2])) and np.isnan(rr[2]) and rr[3] == 0
+    assert np.isnan(v[3, 299]) and np.all(v[3, :299] == 0)
+    assert np.all(v[4] == 1.0) and abs(rr[4] * 3e38 - 1) < 1e-6      # fp32 holds 1 / 3e38 in 21 bits
     assert abs(rr[1] - 1e3) <= 1e3 * 4 * U and abs(rr[5] - 1e3) <= 1e3 * 4 * U
     assert np.all(np.abs(v[5] - 1e-27) <= O.HALF["e4m3"] * 1.01e-27)
     assert np.all(np.isfinite(v[[0, 6]]))
