@@ -257,9 +257,9 @@ __device__ __forceinline__ void for_each(F&& f) {
 // row's number itself); the loads permute their source addresses, as LDS is
 // filled in the order of the lanes.  Which k of a block a lane takes does not
 // matter, as long as both operands agree: it has one scale.
-template <int BM, int BN, int WM, int WN, int STAGES, int FA, int FB, bool EXACT>
+template <int BM, int BN, int WM, int WN, int FA, int FB, bool EXACT>
 __global__ __launch_bounds__(64 * WM * WN) void k_mul8_tile(const Mul8Args a, const uint32_t tiles_m, const uint32_t tiles_n) {
-    constexpr int kWaves = WM * WN;
+    constexpr int kWaves = WM * WN, STAGES = 2;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;      // 32 x 32 pieces of a wave
     constexpr int LA = BM / 8 / kWaves, LB = BN / 8 / kWaves; // loads of a wave for a stage
     constexpr uint32_t kStage = (BM + BN) * kBlock8;
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mul8_tile(const Mul8Args a, co
                 constexpr int S = decltype(step)::value;
                 if constexpr (S == 0) read_y(stage, Second());
                 if constexpr (S + R - 1 == kSteps) {
-                    stage_ready<(STAGES - 2) * (LA + LB)>();   // (scale words are on their way besides, behind the first blocks)
+                    stage_ready<0>();
                     words(((kb + 1) >> 2) + 1, (kb + 1 & 3) == 3);
                     free_stage = stage;
                     stage = stage + 1 == STAGES ? 0 : stage + 1;
@@ -707,7 +707,7 @@ __global__ __launch_bounds__(512) void k_mul8_small(const Mul8Args a, const uint
             const int stage = kb % STAGES;
             // this block has arrived, the one before it has been read
             stage_ready<2 * (STAGES - 2)>();
-            words((kb >> 2) + 1, (kb & 3) == 3);
+            if ((kb & 3) == 0) words((kb >> 2) + 1, true);
             load((kb + STAGES - 1) % STAGES, kb + STAGES - 1);
             const unsigned char* w = reinterpret_cast<const unsigned char*>(lds) + kWords + (kb >> 2 & 1) * (BM + BN) * 4 + (kb & 3);
             const int ex = w[4 * (wm * 32 + row)], ey = w[4 * (BM + wn * 32 + row)];
@@ -757,11 +757,11 @@ __global__ __launch_bounds__(256) void k_mul8_join(const Mul8Args a) {
     store4(a, r, c, sum);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int FA, int FB, bool EXACT>
+template <int BM, int BN, int WM, int WN, int FA, int FB, bool EXACT>
 hipError_t launch_tile(const Mul8Args& a, hipStream_t s) {
     const uint32_t tm = (uint32_t)((a.m + BM - 1) / BM), tn = (uint32_t)((a.n + BN - 1) / BN);
-    constexpr int bytes = STAGES * (BM + BN) * kBlock8 + 2 * (BM + BN) * 4;
-    const auto k = k_mul8_tile<BM, BN, WM, WN, STAGES, FA, FB, EXACT>;
+    constexpr int bytes = 2 * (BM + BN) * kBlock8 + 2 * (BM + BN) * 4;
+    const auto k = k_mul8_tile<BM, BN, WM, WN, FA, FB, EXACT>;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
@@ -810,9 +810,9 @@ hipError_t launch_kind(int kind, const Mul8Args& a, hipStream_t s) {
         if (a.m <= 32) return launch_few<2, FA, FB, EXACT>(a, s);
         return launch_few<4, FA, FB, EXACT>(a, s);
     case MUL8_64: return launch_small<FA, FB, EXACT>(a, s);
-    case MUL8_128: return launch_tile<128, 128, 2, 2, 2, FA, FB, EXACT>(a, s);
+    case MUL8_128: return launch_tile<128, 128, 2, 2, FA, FB, EXACT>(a, s);
     default:
-        if constexpr (EXACT) return launch_tile<256, 256, 2, 4, 2, FA, FB, EXACT>(a, s);
+        if constexpr (EXACT) return launch_tile<256, 256, 2, 4, FA, FB, EXACT>(a, s);
         else return launch_big<FA, FB>(a, s);
     }
 }

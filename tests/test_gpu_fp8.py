@@ -441,7 +441,7 @@ PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 1000, 1000), (2, 300, 129), (15, 17, 64
             (64, 4096, 130), (65, 1, 1025), (100, 3, 5000), (128, 128, 128), (129, 255, 384), (200, 777, 1030), (256, 256, 256),
             (257, 513, 640), (300, 500, 0), (511, 1, 77), (600, 1300, 1500), (1, 5, 20000), (48, 96, 30000), (1024, 512, 8200),
             # every size of tile, whole and with ragged ends, and sums in parts
-            (2048, 2048, 256), (2049, 2100, 300), (4100, 4001, 129), (4096, 4096, 128), (4099, 4103, 1152), (2300, 4600, 1400), (513, 520, 33000)]
+            (2048, 2048, 256), (2049, 2100, 300), (4100, 4001, 129), (4096, 4096, 128), (4099, 4103, 1152), (2300, 4600, 1400), (4000, 4090, 1930), (513, 520, 33000)]
 
 
 @pytest.mark.parametrize("mnk", PRODUCTS)
@@ -532,6 +532,46 @@ def test_product_without_terms():
     F.matmul(a, b, c)
     assert torch.all(c == 0)
     F.matmul(F.Matrix8(0, 9), F.Matrix8(7, 9), torch.empty(0, 7, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 bytes and elements: what lies at their ends."""
+    rows, cols = 33000, 131200
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, cols, device="cuda").bfloat16()
+    x[:, -5:] = torch.randn(rows, 5, device="cuda").bfloat16()
+    a, b = F.Matrix8(rows, cols), F.Matrix8(cols, rows)
+    F.quantize(x, rows=a, cols=b)
+    v = np64(x[-130:])
+    codes, e = O.encode(v, "e4m3")
+    np.testing.assert_array_equal(a.codes[-130:].view(torch.uint8).cpu().numpy(), codes)
+    byte, has = O.grouped(e)
+    np.testing.assert_array_equal(a.scales[:, -130:].cpu().numpy()[has], byte[has])
+    codes, e = O.encode(np64(x[:, -140:]).T, "e4m3")
+    np.testing.assert_array_equal(b.codes[-140:].view(torch.uint8).cpu().numpy(), codes)
+    t = F.Matrix8(cols, rows)
+    F.transpose(a, t)
+    held = O.values(a.codes.view(torch.uint8)[:, -128:].cpu().numpy(), a.scales[-1:, :, cols // 128 % 4 - 1:].cpu().numpy(), 128, "e4m3")
+    codes, _ = O.encode(held.T, "e4m3")
+    np.testing.assert_array_equal(t.codes[-128:].view(torch.uint8).cpu().numpy(), codes)
+    del t
+    # products of the last rows, each kind of kernel by the number of rows
+    va = O.values(a.codes[-2:].view(torch.uint8).cpu().numpy(), a.scales[:, -2:].cpu().numpy(), cols, "e4m3")
+    want, most = va @ va.T, np.abs(va) @ np.abs(va).T
+    for many in (2, 100, 700):
+        c = torch.empty(many, many, device="cuda")
+        F.matmul(a.between(rows - many, rows), a.between(rows - many, rows), c)
+        assert np.all(np.abs(np64(c)[-2:, -2:] - want) <= (cols + 64) * 2 * U * most)
+    out, w = torch.empty_like(x), torch.ones(cols, device="cuda")
+    F.rms_norm(x, w, 1e-6, out8=a, out=out)
+    h = O.rms_norm(v[-3:], np.ones(cols), 1e-6)[1]
+    assert np.all(np.abs(np64(out[-3:]) - h) <= HALF["bf16"] * (1 + 2.0 ** -10) * np.abs(h))
+    big = torch.empty(66000, 66000, dtype=torch.bfloat16, device="cuda")       # 2^32 elements of C
+    m = F.Matrix8(66000, 130)
+    m.codes.view(torch.uint8)[-1, :130] = int(O.nearest(1.0, "e4m3"))
+    m.scales[0, -1, :2] = 127
+    F.matmul(m, m, big)
+    assert float(big[-1, -1]) == 130.0 and float(big[-1, -2]) == 0.0 and float(big[0, 0]) == 0.0
 
 
 # ------------------------------------------------------------ together
