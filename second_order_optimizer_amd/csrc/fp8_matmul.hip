@@ -173,12 +173,19 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
 // 16 bytes of each lane from memory into LDS, without registers between: to
 // `lds` (the wave's, in bytes) + 16 lane, from `base` + `off`.  Written out so
 // that the reads of one stage do not wait for the loads of the next; the wait
-// is stage_ready's.
+// is stage_ready's.  A memory instruction must not read a scalar register within
+// five wait states of the vector instruction that wrote it (v_readfirstlane of
+// `uniform`, v_readlane of a spill): the hardware does not wait, and the compiler
+// does not look in here.  So the load reads a copy that a scalar instruction
+// made, for which the hardware does; the copy is the wait that m0 needs as well
+// (8192^3: 381 us, with s_nop 4 in its place 391).
 __device__ __forceinline__ void dma16(uint32_t lds, uint64_t base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
+    uint64_t from;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0" : "=&s"(from) : "s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(uint32_t lds, uint64_t base, uint32_t off) {   // 4 bytes of each lane
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
+    uint64_t from;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0" : "=&s"(from) : "s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
 }
 // Every load of this wave but the last N has arrived, its reads too, and so
 // have those of the workgroup's other waves.

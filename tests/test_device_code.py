@@ -1,0 +1,102 @@
+"""The library's own gfx950 code, read back: what its hand-written instructions
+owe the hardware and the compiler does not see to."""
+import glob
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from second_order_optimizer_amd import build as B
+
+OBJDUMP = os.path.join(os.path.dirname(os.path.realpath(B.HIPCC)), "..", "llvm", "bin", "llvm-objdump")
+OBJDUMP = OBJDUMP if os.path.exists(OBJDUMP) else "/opt/rocm/llvm/bin/llvm-objdump"
+MEMORY = re.compile(r"(global|buffer|flat|scratch)_")
+SCALARS = re.compile(r"\bs(?:\[(\d+):(\d+)\]|(\d+)\b)|\bvcc\b")
+WAIT_STATES = 5      # from a vector instruction's write of a scalar register to a memory instruction's read of it
+
+
+def kernels(text):
+    """(name, [instruction, ...]) of a disassembly."""
+    name, body = None, []
+    for line in text.splitlines():
+        head = re.match(r"[0-9a-f]+ <(.+)>:$", line)
+        if head:
+            if body:
+                yield name, body
+            name, body = head.group(1), []
+        elif line.startswith("\t") and name:
+            body.append(line.split("//")[0].strip())
+    if body:
+        yield name, body
+
+
+def scalars(operands):
+    found = set()
+    for low, high, one in SCALARS.findall(operands):
+        found |= {"vcc"} if not (low or one) else set(range(int(low or one), int(high or one) + 1))
+    return found
+
+
+def written(instruction):
+    """Scalar registers that a vector instruction writes: its first operand, and
+    the carry or flag behind it where an instruction has one."""
+    op, _, operands = instruction.partition(" ")
+    if not op.startswith("v_"):
+        return set()
+    parts = re.split(r",\s*(?![^\[]*\])", operands)
+    return scalars(parts[0]) | (scalars(parts[1]) if "_co_" in op or "div_scale" in op else set())
+
+
+def too_near(body):
+    """Memory instructions within five wait states of a vector instruction that
+    writes a scalar register of theirs."""
+    bad = []
+    for i, ins in enumerate(body):
+        if not MEMORY.match(ins):
+            continue
+        used, states = scalars(ins.partition(" ")[2]), 0
+        for back in range(i - 1, -1, -1):
+            if states >= WAIT_STATES or not used:
+                break
+            if written(body[back]) & used:
+                bad.append(f"{states} states: {body[back]} | {ins}")
+                break
+            wait = re.match(r"s_nop (0x[0-9a-f]+|\d+)", body[back])
+            states += int(wait.group(1), 0) + 1 if wait else 1
+    return bad
+
+
+def test_the_scan_itself():
+    near = ["v_readfirstlane_b32 s1, v5", "s_mov_b32 m0, s7", "s_nop 0", "global_load_lds_dwordx4 v2, s[0:1]"]
+    assert len(too_near(near)) == 1
+    assert not too_near(near[:2] + ["s_nop 3"] + near[3:])
+    assert len(too_near(near[:2] + ["s_nop 2"] + near[3:])) == 1
+    assert not too_near(near[:3] + ["global_load_lds_dwordx4 v2, s[2:3]"])
+    assert not too_near(near[:2] + ["s_mov_b64 s[8:9], s[0:1]", "global_load_lds_dwordx4 v2, s[8:9]"])      # a copy
+    assert not too_near(["s_mov_b32 s1, s5"] + near[1:])
+    assert len(too_near(["v_cmp_lt_i32_e64 s[0:1], v1, v2", "buffer_load_dword v1, v2, s[0:3], 0 offen"])) == 1
+    assert not too_near(["v_add_f32 v0, s1, v2", "global_load_dword v1, v2, s[0:1]"])      # a read
+    assert len(too_near(["v_add_co_u32_e64 v0, s[0:1], v1, v2", "global_load_dword v1, v2, s[0:1]"])) == 1
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
+def test_memory_instructions_wait_for_scalar_bases(tmp_path):
+    """A memory instruction that reads a scalar register which a vector
+    instruction wrote needs five wait states between; the hardware does not wait,
+    and the compiler does not look into inline assembly."""
+    if not os.path.exists(B.LIB):
+        B.build()
+    lib = shutil.copy(B.LIB, tmp_path)
+    subprocess.run([OBJDUMP, "--offloading", lib], cwd=tmp_path, check=True, capture_output=True)
+    loads, bad = 0, {}
+    for part in glob.glob(str(tmp_path / "*gfx950")):
+        text = subprocess.run([OBJDUMP, "-d", part], check=True, capture_output=True, text=True).stdout
+        for name, body in kernels(text):
+            loads += sum("load_lds" in ins for ins in body)
+            near = too_near(body)
+            if near:
+                bad[name] = near
+    assert loads > 100, "the loads into LDS are there"
+    assert not bad, "\n".join(f"{k}: {len(v)}, e.g. {v[0]}" for k, v in bad.items())
