@@ -29,6 +29,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
+import operator
 import struct
 from typing import Optional, Sequence, Tuple
 
@@ -283,9 +285,16 @@ class Weights8(_Bound):
         return Matrix8(d.rows, d.cols, "e4m3", codes=codes, scales=scales)
 
     def bind(self, weights):
-        """The weights from now on: contiguous tensors of the plan's sizes."""
-        self._call(lib().shampoo_weights8_bind_weights, self._addresses(weights, self.want, "weights"))
-        self._held = list(weights)
+        """The weights from now on: contiguous tensors of the plan's shapes, flat
+        ones, or ones of more dimensions that are the plan's two taken apart
+        (out x in x 3 x 3 for out rows)."""
+        weights = list(weights)
+        at = self._addresses(weights, self.want, "weights")
+        for i, (t, (r, c)) in enumerate(zip(weights, self.shapes)):
+            if t is not None and t.dim() > 1 and r not in itertools.accumulate(t.shape[:-1], operator.mul):
+                raise ValueError(f"weights[{i}] must have {r} rows of {c} elements, got {tuple(t.shape)}")
+        self._call(lib().shampoo_weights8_bind_weights, at)
+        self._held = weights
 
     def refresh(self):
         """Copies of the bound weights as they are now (one launch)."""

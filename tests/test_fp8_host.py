@@ -308,3 +308,38 @@ def test_norm_gradient_against_differences():
         d = np.zeros_like(w)
         d[i] = h
         assert abs((f(z, w + d) - f(z, w - d)) / (2 * h) - dw[i]) < 1e-7
+
+
+# ------------------------------------------------------------ weights as their plan has them
+def unbound(shapes, device="cpu"):
+    """A Weights8 whose binding can be checked without a GPU: no library, no state."""
+    from second_order_optimizer_amd import fp8 as F
+    w = F.Weights8.__new__(F.Weights8)
+    w.shapes = list(shapes)
+    w.want = [(r * c, 0) for r, c in shapes]
+    w.device, w._types = torch.device(device), (torch.float32, torch.bfloat16, torch.float16)
+    w.calls = []
+    w._call = lambda fn, *args: w.calls.append(fn.__name__)
+    w._held = None
+    return w
+
+
+@pytest.mark.parametrize("planned,shape", [((4, 6), (6, 4)), ((4, 6), (3, 8)), ((4, 6), (2, 12)), ((4, 6), (6, 2, 2)), ((2, 12), (3, 2, 4)),
+                                           ((1, 24), (4, 6, 1)), ((24, 1), (2, 12)), ((4, 0), (0, 7)), ((5, 0), (4, 0))])
+def test_bind_refuses_other_shapes(planned, shape):
+    """As many elements in other rows would be copied as rows that they are not."""
+    w = unbound([(3, 3), planned])
+    with pytest.raises(ValueError, match=r"weights\[1\]"):
+        w.bind([torch.zeros(3, 3), torch.zeros(shape)])
+    assert not w.calls and w._held is None
+
+
+@pytest.mark.parametrize("planned,shape", [((4, 6), (4, 6)), ((4, 6), (24,)), ((4, 6), (4, 2, 3)), ((4, 6), (2, 2, 6)), ((4, 6), (4, 2, 3, 1)),
+                                           ((4, 6), (1, 4, 6)), ((1, 24), (1, 4, 6)), ((24, 1), (4, 6, 1)), ((0, 5), (0, 5)), ((5, 0), (5, 0)), ((1, 1), ())])
+def test_bind_takes_the_plans_rows(planned, shape):
+    """The plan's shape, its elements in one dimension, and more dimensions that
+    are its rows and columns taken apart."""
+    w = unbound([planned])
+    t = torch.zeros(shape)
+    w.bind([t])
+    assert w.calls == ["shampoo_weights8_bind_weights"] and w._held[0] is t
