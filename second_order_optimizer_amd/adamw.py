@@ -206,8 +206,9 @@ class AdamW(_Bound):
         step reads when it runs.  clip: scale the gradients by the coefficient
         of its last compute, and skip the step where its norm is not finite.
         The gradients are those before clipping: not ones that clip_into has
-        scaled in place.  copies8: 8-bit copies of weights (fp8.Weights8) that
-        are refreshed behind it."""
+        scaled in place.  copies8: 8-bit copies (fp8.Weights8) of some or all
+        of the bound weights, or of parts of them, that are refreshed behind
+        it; it is refused where one is bound to another tensor."""
         dev_lr = None
         if isinstance(lr, self.torch.Tensor):
             if lr.dtype != self.torch.float32 or lr.numel() != 1 or lr.device != self.device:
@@ -215,6 +216,8 @@ class AdamW(_Bound):
             dev_lr, lr = lr.data_ptr(), 0.0
         if clip is not None and (clip.device != self.device or not clip.computed):
             raise ValueError(f"clip must be on {self.device} and have computed a norm")
+        if copies8 is not None:
+            copies8._stepped(self._held[0])
         self._call(lib().shampoo_adamw_step, lr, dev_lr, None if clip is None else clip.record_ptr)
         if copies8 is not None:
             copies8.refresh()

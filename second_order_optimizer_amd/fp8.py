@@ -27,6 +27,7 @@ library has not been built -- there is no fallback.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 import itertools
@@ -295,6 +296,30 @@ class Weights8(_Bound):
                 raise ValueError(f"weights[{i}] must have {r} rows of {c} elements, got {tuple(t.shape)}")
         self._call(lib().shampoo_weights8_bind_weights, at)
         self._held = weights
+        self._spans = [(i, t.data_ptr(), t.data_ptr() + t.nbytes) for i, t in enumerate(weights)
+                       if t is not None and t.nbytes]
+
+    def _stepped(self, params):
+        """Refuses params, the tensors of a step, that a bound weight is not one
+        or a part of: its copies would stay those of a tensor left behind."""
+        if self._held is None:
+            raise ValueError("copies8: no weights are bound")
+        ends = {}
+        for p in params or ():
+            if p is not None:
+                at = p.data_ptr()
+                ends[at] = max(at + p.nbytes, ends.get(at, 0))
+        starts = reach = None
+        for i, low, high in self._spans:
+            if ends.get(low, 0) >= high:
+                continue
+            if starts is None:       # parts of tensors: how far memory goes from each start on
+                starts = sorted(ends)
+                reach = list(itertools.accumulate((ends[a] for a in starts), max))
+            k = bisect.bisect_right(starts, low) - 1
+            if k < 0 or reach[k] < high:
+                raise ValueError(f"copies8: weights[{i}] is not of the tensors that this step changes; bind the "
+                                 "present ones, or call refresh() where several steps share the copies")
 
     def refresh(self):
         """Copies of the bound weights as they are now (one launch)."""

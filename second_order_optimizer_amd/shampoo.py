@@ -414,8 +414,11 @@ class Shampoo(Plan):
 
     def step(self, params, grads, step: int, cadence: int, sparse=None, copies8=None):
         """One optimizer step (shampoo_step): statistics, roots when
-        step % cadence == 0, apply.  copies8: 8-bit copies of weights
-        (fp8.Weights8) that are refreshed behind it."""
+        step % cadence == 0, apply.  copies8: 8-bit copies (fp8.Weights8) of
+        some or all of params, or of parts of them, that are refreshed behind
+        it; it is refused where one is bound to another tensor."""
+        if copies8 is not None:
+            copies8._stepped(params)
         self._step(params, grads, step, cadence, sparse)
         if copies8 is not None:
             copies8.refresh()

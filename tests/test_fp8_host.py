@@ -343,3 +343,63 @@ def test_bind_takes_the_plans_rows(planned, shape):
     t = torch.zeros(shape)
     w.bind([t])
     assert w.calls == ["shampoo_weights8_bind_weights"] and w._held[0] is t
+
+
+# ------------------------------------------------------------ copies behind a step
+class Stepped(S.Shampoo):
+    """Shampoo's and AdamW's step() around steps that only say that they ran."""
+
+    def __init__(self):
+        self.ran = 0
+
+    def _step(self, *args):
+        self.ran += 1
+
+
+def adamw_over(params):
+    from second_order_optimizer_amd import adamw as A
+    opt = A.AdamW.__new__(A.AdamW)
+    opt.torch, opt.device, opt.ran = torch, torch.device("cpu"), 0
+    opt._held = [params, None]
+
+    def call(fn, *args):
+        opt.ran += 1
+    opt._call = call
+    return opt
+
+
+def both_steps(params, copies):
+    """The steps that ran, of Shampoo and of AdamW, before either's refusal."""
+    out = []
+    s = Stepped()
+    a = adamw_over(params)
+    for opt, step in ((s, lambda: s.step(params, [None] * len(params), 0, 1, copies8=copies)), (a, lambda: a.step(1e-3, copies8=copies))):
+        try:
+            step()
+            out.append(opt.ran)
+        except ValueError:
+            assert opt.ran == 0, "refused before the step, not behind it"
+            out.append(None)
+    return out
+
+
+def test_copies_are_of_the_stepped_weights():
+    """Copies of tensors that the step does not change would stay those of old
+    values; a part of a stepped tensor is one."""
+    a, b, other = torch.zeros(4, 6), torch.zeros(8, 3), torch.zeros(4, 6)
+    w = unbound([(4, 6), (8, 3)])
+    assert both_steps([a, b], w) == [None, None]               # nothing bound
+    w.bind([a, b])
+    assert both_steps([a, b], w) == [1, 1]
+    assert both_steps([other, b, a], w) == [1, 1]
+    assert w.calls.count("shampoo_weights8_refresh") == 4
+    assert both_steps([other, b], w) == [None, None]           # another tensor in a's place
+    assert both_steps([other, other], w) == [None, None]
+    assert both_steps([a.clone(), b.clone()], w) == [None, None]
+    w.bind([a.view(-1), b.view(8, 3, 1)])
+    assert both_steps([a, b], w) == [1, 1]
+    part = unbound([(2, 6), (0, 6)])
+    part.bind([a[1:3], torch.zeros(0, 6)])
+    assert both_steps([b, a], part) == [1, 1]
+    assert both_steps([a[:2], b], part) == [None, None]        # its second row is not stepped
+    assert both_steps([a[1:3], b], part) == [1, 1]
