@@ -506,31 +506,36 @@ __global__ __launch_bounds__(64 * W * bwd_groups(W)) void k_norm_bwd(const NormB
 }
 
 // dw: the slots' sums, in the order of the slots; 32 columns and 32 runs of
-// slots to a workgroup.
+// slots to a workgroup, which takes further columns where a row has more than
+// kDwGroups of them (a launch of 2^32 threads or more would wrap).
+constexpr int64_t kDwGroups = 1 << 20;
 __global__ __launch_bounds__(1024) void k_norm_dw(const NormBwdArgs a) {
     __shared__ float s[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + x;
     const int per = (a.slots + 31) / 32, from = y * per, to = from + per < a.slots ? from + per : a.slots;
-    float sum = 0.f;
-    if (c < a.dim) {
-        const float* p = a.partials + c;
-        int i = from;
-        for (; i + 8 <= to; i += 8) {       // eight loads on their way together
-            float v[8];
+    for (int64_t first = (int64_t)blockIdx.x * 32; first < a.dim; first += kDwGroups * 32) {
+        const int64_t c = first + x;
+        float sum = 0.f;
+        if (c < a.dim) {
+            const float* p = a.partials + c;
+            int i = from;
+            for (; i + 8 <= to; i += 8) {       // eight loads on their way together
+                float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(i + k) * a.dim];
+                for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)(i + k) * a.dim];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k];
+                for (int k = 0; k < 8; ++k) sum += v[k];
+            }
+            for (; i < to; ++i) sum += p[(int64_t)i * a.dim];
         }
-        for (; i < to; ++i) sum += p[(int64_t)i * a.dim];
-    }
-    s[y][x] = sum;
-    __syncthreads();
-    if (y == 0 && c < a.dim) {
+        s[y][x] = sum;
+        __syncthreads();
+        if (y == 0 && c < a.dim) {
 #pragma unroll
-        for (int k = 1; k < 32; ++k) sum += s[k][x];
-        a.dw[c] = a.accumulate ? a.dw[c] + sum : sum;
+            for (int k = 1; k < 32; ++k) sum += s[k][x];
+            a.dw[c] = a.accumulate ? a.dw[c] + sum : sum;
+        }
+        if (first + kDwGroups * 32 < a.dim) __syncthreads();     // s has been read
     }
 }
 
@@ -682,7 +687,8 @@ hipError_t launch_norm_bwd(int gt, int zt, const NormBwdArgs& a, hipStream_t s) 
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dw) return e;
-    k_norm_dw<<<(uint32_t)((a.dim + 31) / 32), 1024, 0, s>>>(a);
+    const int64_t groups = (a.dim + 31) / 32;
+    k_norm_dw<<<(uint32_t)(groups < kDwGroups ? groups : kDwGroups), 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
