@@ -178,7 +178,11 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
 // `uniform`, v_readlane of a spill): the hardware does not wait, and the compiler
 // does not look in here.  So the load reads a copy that a scalar instruction
 // made, for which the hardware does; the copy is the wait that m0 needs as well
-// (8192^3: 381 us, with s_nop 4 in its place 391).
+// (8192^3: 381 us, with s_nop 4 in its place 391).  m0 is a register that the
+// compiler reserves and may be told of, with a warning: nothing that it writes
+// itself in these kernels uses m0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(uint32_t lds, uint64_t base, uint32_t off) {
     uint64_t from;
     asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0" : "=&s"(from) : "s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
@@ -187,6 +191,7 @@ __device__ __forceinline__ void dma4(uint32_t lds, uint64_t base, uint32_t off) 
     uint64_t from;
     asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0" : "=&s"(from) : "s"(lds), "v"(off), "s"(uniform(base)) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // Every load of this wave but the last N has arrived, its reads too, and so
 // have those of the workgroup's other waves.
 template <int N>

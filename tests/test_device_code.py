@@ -81,22 +81,40 @@ def test_the_scan_itself():
     assert len(too_near(["v_add_co_u32_e64 v0, s[0:1], v1, v2", "global_load_dword v1, v2, s[0:1]"])) == 1
 
 
+def disassembled(tmp_path):
+    """(name, [instruction, ...]) of every kernel of the built library."""
+    if not os.path.exists(B.LIB):
+        B.build()
+    lib = shutil.copy(B.LIB, tmp_path)
+    subprocess.run([OBJDUMP, "--offloading", lib], cwd=tmp_path, check=True, capture_output=True)
+    for part in glob.glob(str(tmp_path / "*gfx950")):
+        yield from kernels(subprocess.run([OBJDUMP, "-d", part], check=True, capture_output=True, text=True).stdout)
+
+
 @pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
 def test_memory_instructions_wait_for_scalar_bases(tmp_path):
     """A memory instruction that reads a scalar register which a vector
     instruction wrote needs five wait states between; the hardware does not wait,
     and the compiler does not look into inline assembly."""
-    if not os.path.exists(B.LIB):
-        B.build()
-    lib = shutil.copy(B.LIB, tmp_path)
-    subprocess.run([OBJDUMP, "--offloading", lib], cwd=tmp_path, check=True, capture_output=True)
     loads, bad = 0, {}
-    for part in glob.glob(str(tmp_path / "*gfx950")):
-        text = subprocess.run([OBJDUMP, "-d", part], check=True, capture_output=True, text=True).stdout
-        for name, body in kernels(text):
-            loads += sum("load_lds" in ins for ins in body)
-            near = too_near(body)
-            if near:
-                bad[name] = near
+    for name, body in disassembled(tmp_path):
+        loads += sum("load_lds" in ins for ins in body)
+        near = too_near(body)
+        if near:
+            bad[name] = near
     assert loads > 100, "the loads into LDS are there"
     assert not bad, "\n".join(f"{k}: {len(v)}, e.g. {v[0]}" for k, v in bad.items())
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
+def test_loads_into_lds_have_m0_to_themselves(tmp_path):
+    """Each sets m0 two instructions before it, and nothing else in its kernel
+    uses m0."""
+    loads = 0
+    for name, body in disassembled(tmp_path):
+        at = [i for i, ins in enumerate(body) if "load_lds" in ins]
+        if at:
+            loads += len(at)
+            assert all(body[i - 2].startswith("s_mov_b32 m0, ") for i in at), name
+            assert sum("m0" in ins for ins in body) == len(at), name
+    assert loads > 100
