@@ -304,18 +304,16 @@ class Weights8(_Bound):
         or a part of: its copies would stay those of a tensor left behind."""
         if self._held is None:
             raise ValueError("copies8: no weights are bound")
-        ends = {}
-        for p in params or ():
-            if p is not None:
-                at = p.data_ptr()
-                ends[at] = max(at + p.nbytes, ends.get(at, 0))
+        params = [p for p in params or () if p is not None]
+        sizes = {p.data_ptr(): p.nbytes for p in params}
         starts = reach = None
         for i, low, high in self._spans:
-            if ends.get(low, 0) >= high:
+            if sizes.get(low, 0) >= high - low:
                 continue
             if starts is None:       # parts of tensors: how far memory goes from each start on
-                starts = sorted(ends)
-                reach = list(itertools.accumulate((ends[a] for a in starts), max))
+                spans = sorted((p.data_ptr(), p.data_ptr() + p.nbytes) for p in params)
+                starts = [at for at, _ in spans]
+                reach = list(itertools.accumulate((end for _, end in spans), max))
             k = bisect.bisect_right(starts, low) - 1
             if k < 0 or reach[k] < high:
                 raise ValueError(f"copies8: weights[{i}] is not of the tensors that this step changes; bind the "

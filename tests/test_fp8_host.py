@@ -392,7 +392,8 @@ def test_copies_are_of_the_stepped_weights():
     w.bind([a, b])
     assert both_steps([a, b], w) == [1, 1]
     assert both_steps([other, b, a], w) == [1, 1]
-    assert w.calls.count("shampoo_weights8_refresh") == 4
+    assert both_steps([a, b, a[:1], b[:2]], w) == [1, 1]       # views that begin where they do
+    assert w.calls.count("shampoo_weights8_refresh") == 6
     assert both_steps([other, b], w) == [None, None]           # another tensor in a's place
     assert both_steps([other, other], w) == [None, None]
     assert both_steps([a.clone(), b.clone()], w) == [None, None]
