@@ -651,15 +651,18 @@ int shampoo_quantize8(const void* x, int32_t type, int64_t pitch, int64_t nrows,
 /* The transpose of an 8-bit matrix, its values scaled anew along the other
  * side: what dW needs of an activation that was kept in 8 bits.  A value is
  * rounded again only where the new scale leaves it below the format's normal
- * range (2^-14 of the block's largest for e4m3, 2^-29 for e5m2, or less).
- * Errors: as above. */
+ * range (2^-14 of the block's largest for e4m3, 2^-29 for e5m2, or less), and
+ * where e4m3 becomes e5m2, which has one digit less.  A value of 2^128 or more
+ * (what the largest fp32 numbers round to) counts as infinite.  Errors: as
+ * above. */
 int shampoo_transpose8(const shampoo_matrix8* m, const shampoo_matrix8* out, void* stream);
 
 /* Root-mean-square norm of every row, with the residual's addition before it
  * and an output in 8 bits:
  *   z = x + residual, rounded to the residual's type and written to `total`
  *   r = 1 / sqrt(mean(z^2) + eps),  h = z r w
- * in 64 bits, h and r rounded to fp32 and h then to its outputs.  Without a residual z is x and total is not written.
+ * in 64 bits, h and r rounded to fp32 and h then to its outputs.  Without a
+ * residual z is x and total is not written.
  * total may be the residual or x itself (the same address, pitch and type).
  * h goes to out8 (e4m3, blocks along the row), to `out`, or to both. */
 typedef struct {
@@ -676,7 +679,7 @@ typedef struct {
     double eps;                    /* 2^-120 to 2^120 */
 } shampoo_rms_norm_args;
 /* Errors: SHAMPOO_E_ARG, SHAMPOO_E_UNSUPPORTED (out8 in e5m2; 2^32 or more
- * threads: 2^22 rows where dim > 8192, 2^24 at least otherwise),
+ * threads: 2^22 rows where dim > 8192, 2^23 where dim > 4096, 2^24 at least otherwise),
  * SHAMPOO_E_HIP. */
 int shampoo_rms_norm8(const shampoo_rms_norm_args* args, void* stream);
 
@@ -707,11 +710,14 @@ int shampoo_rms_norm8_backward(const shampoo_rms_norm_grad_args* args, void* wor
 
 /* c (a.rows x b.rows, shampoo_dtype) = A B^T, or c + A B^T (accumulate = 1), for
  * 8-bit matrices with the same number of columns.  Sums are those of fp32
- * where c is fp32; where it has 16 bits, eight products at a time are added with
- * those below 2^-13 of the largest cut off, which leaves some 2e-5 of the
- * result (a fiftieth of bf16's rounding).  fp32: a factor below 2^-126 may count
- * as 0, one of 2^128 or more counts as infinite.  A sum that leaves the range of c's type becomes infinite.  workspace: as above, NULL
- * where shampoo_matmul8_workspace says 0 bytes.  Errors: SHAMPOO_E_ARG,
+ * where c is fp32; where it has 16 bits, eight products at a time are added, each
+ * cut off below 2^-13 of the largest of them, at most 7 * 2^-13 of it in all: some
+ * 2e-5 of the result on values of a network (a fiftieth of bf16's rounding), and
+ * more of it where large products cancel, for which c in fp32 is the way.  fp32:
+ * a factor (code times scale) below 2^-126 may count as 0, one of 2^128 or more
+ * counts as infinite.  A sum that leaves the range of c's type, or on the way
+ * that of fp32, becomes infinite.  workspace: as above, NULL where
+ * shampoo_matmul8_workspace says 0 bytes.  Errors: SHAMPOO_E_ARG,
  * SHAMPOO_E_STATE (workspace too small), SHAMPOO_E_UNSUPPORTED (2^22 or more
  * tiles; rows more than 2^23 bytes apart), SHAMPOO_E_HIP. */
 int shampoo_matmul8_workspace(int64_t m, int64_t n, int64_t k, int32_t type, size_t* bytes);

@@ -18,7 +18,9 @@ activations, gradients and weights into 8 bits.
 
 A value in 8 bits is an e4m3 or e5m2 code times a power of two that 128
 neighbours along a row share (weights: 128 x 128).  The gradients take the
-rounding to 8 bits as the identity.
+rounding to 8 bits as the identity.  The calls record nothing for autograd: they
+take tensors that require a gradient as values, and their outputs carry none; a
+backward pass is made of the calls above.
 
 Tensors are 2-D with neighbouring elements in a row (any row pitch, any start);
 outputs are given.  Every call runs on the current stream of its tensors'

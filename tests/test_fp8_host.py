@@ -404,3 +404,9 @@ def test_copies_are_of_the_stepped_weights():
     assert both_steps([b, a], part) == [1, 1]
     assert both_steps([a[:2], b], part) == [None, None]        # its second row is not stepped
     assert both_steps([a[1:3], b], part) == [1, 1]
+
+
+@pytest.mark.parametrize("dim,rows", [(8193, 1 << 22), (8192, 1 << 23), (4097, 1 << 23), (4096, 1 << 24), (2049, 1 << 24), (2048, 1 << 25), (1025, 1 << 25), (1024, 1 << 26)])
+def test_norm_rows_past_a_launch(dim, rows):
+    """The least number of rows whose launch would have 2^32 threads."""
+    assert norm(rows=rows, dim=dim, x=1 << 45, out=1 << 50, x_pitch=dim, out_pitch=dim) == E_UNSUPPORTED

@@ -86,6 +86,23 @@ def test_norm_backward_keeps_what_is_not_finite_to_its_row(dim, rows):
     assert not bool(torch.isfinite(dw[5])) and int((~torch.isfinite(dw)).sum()) == 1
 
 
+def test_transpose_of_the_largest_numbers():
+    """The largest fp32 number rounds to a code that stands for 2^128, which
+    transposes as an infinity: NaN in e4m3, and its neighbours as they were."""
+    for fmt in ("e4m3", "e5m2"):
+        x = torch.ones(130, 200, device="cuda")
+        x[3], x[100, 7], x[129, 199] = 3.4028234663852886e38, -3.4028234663852886e38, 3e38
+        a = Held(130, 200, fmt)
+        F.quantize(x, rows=a.m)
+        v = a.values().T
+        assert v[5, 3] == 2.0 ** 128 and v[7, 100] == -2.0 ** 128 and v[199, 129] < 2.0 ** 128
+        v = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)
+        for to in ("e4m3", "e5m2"):
+            b = Held(200, 130, to)
+            F.transpose(a.m, b.m)
+            b.check(*O.encode(v, to))
+
+
 # ------------------------------------------------------------ product
 def kind_sizes(k):
     """A product of k <= 300 for each kernel: one row of pieces and three of
@@ -240,6 +257,19 @@ def test_what_cancels_down_to_the_cut(mnk, out):
             np.testing.assert_array_equal(np64(c), want)
         else:
             assert np.all(np.abs(np64(c) - want) <= -(-k // 8) * 7 * 2.0 ** -5)
+
+
+def test_nothing_is_recorded_for_autograd():
+    """Inputs that require a gradient are values, and outputs carry none."""
+    x = torch.randn(5, 200, device="cuda", requires_grad=True)
+    gain = torch.ones(200, device="cuda", requires_grad=True)
+    out, r, h8, y = torch.empty(5, 200, device="cuda"), torch.empty(5, device="cuda"), F.Matrix8(5, 200), torch.empty(5, 5, device="cuda")
+    F.rms_norm(x, gain, 1e-6, out=out, out8=h8, rstd=r)
+    F.matmul(h8, h8, y)
+    for t in (out, r, y):
+        assert not t.requires_grad and t.grad_fn is None
+    want = O.rms_norm(np64(x), np64(gain), 1e-6)[1]
+    assert np.all(np.abs(np64(out) - want) <= U * (1 + 2.0 ** -20) * np.abs(want))
 
 
 def test_norm_backward_of_the_longest_row():
