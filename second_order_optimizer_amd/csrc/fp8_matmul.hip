@@ -6,11 +6,12 @@
 // They add products in eights, each cut off below 2^-13 of the largest, and
 // those sums in fp32 (found by products of single powers of two): on normally
 // distributed values 1.5e-5 of the result, with one column in a hundred
-// twentyfold 4.4e-5, a fiftieth of what rounding to bf16 leaves.  fp32: the codes
-// are widened to bf16 with their scale, exactly, and multiplied by the bf16
-// instructions, whose sums are those of fp32 (6e-8 at K = 2048, 2e-7 at 16384),
-// at half the rate: a weight's gradient that is added up over micro-batches
-// keeps its small terms.
+// twentyfold 4.4e-5, a fiftieth of what rounding to bf16 leaves; where large
+// products cancel it is more of what is left.  fp32: the codes are widened to
+// bf16 with their scale, exactly between 2^-126 and 2^128, and multiplied by the
+// bf16 instructions, whose sums are those of fp32 (6e-8 at K = 2048, 2e-7 at
+// 16384), at half the rate: a weight's gradient that is added up over
+// micro-batches keeps its small terms.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -82,7 +83,9 @@ __device__ __forceinline__ i32x8 operand(const Mat8& m, int64_t row, int64_t blo
 }
 
 // Eight codes as bf16 values with their scale applied: exact, as bf16 has the
-// exponents of fp32 and more digits than a code.
+// exponents of fp32 and more digits than a code, but for values below 2^-126,
+// which may become 0, and of 2^128 or more, which become infinite.  The
+// instruction reads the scale's exponent alone: 0 is 2^-127.
 template <int FMT>
 __device__ __forceinline__ bf16x8 widened(int lo, int hi, float scale) {
     bf16x2 q[4];
@@ -108,8 +111,10 @@ __device__ __forceinline__ bf16x8 widened(int lo, int hi, float scale) {
 // their order.  Reading B bounds it, so what counts is how many of its bytes are
 // on their way at once (1 x 8192 x 8192: 13.7 us, 4.9 TB/s, against 19.4 by tiles of
 // 64 x 64; 1 x 4096 x 1024: 3.1 us, latency; 64 x 4096 x 1024: 5.7 us against 6.5, but
-// 13.7 against 11.3 over 4096, where every workgroup reads all of A).  The rows of B stand as the instruction's rows, so that a
-// lane holds four neighbouring columns of C.
+// 13.7 against 11.3 over 4096, where every workgroup reads all of A; each pair on
+// one card, on another 12.2 us, 3.2 and 4.8, and 10.3 by tiles).  The rows of B
+// stand as the instruction's rows, so that a lane holds four neighbouring columns
+// of C.
 template <int MT, int W, int U, int FA, int FB, bool EXACT>
 __global__ __launch_bounds__(64 * W) void k_mul8_few(const Mul8Args a) {
     __shared__ f32x4 s_sum[W][MT][64];
@@ -271,8 +276,8 @@ __device__ __forceinline__ void for_each(F&& f) {
 // row's number itself); the loads permute their source addresses, as LDS is
 // filled in the order of the lanes.  Which k of a block a lane takes does not
 // matter, as long as both operands agree: it has one scale.  128 x 128 by four
-// waves (two workgroups on a CU), and 256 x 256 by eight for fp32 results: 759 us
-// at 8192^3, 1.45 PFLOP/s, the library's bf16 product 680.
+// waves (two workgroups on a CU), and 256 x 256 by eight for fp32 results: 773 us
+// at 8192^3, 1.42 PFLOP/s, the library's bf16 product 765.
 template <int BM, int BN, int WM, int WN, int FA, int FB, bool EXACT>
 __global__ __launch_bounds__(64 * WM * WN) void k_mul8_tile(const Mul8Args a, const uint32_t tiles_m, const uint32_t tiles_n) {
     constexpr int kWaves = WM * WN, STAGES = 2;
@@ -501,9 +506,9 @@ __device__ __forceinline__ void products_done() { asm volatile("s_nop 15\n\ts_no
 // are all that is held.  The halves that a block takes first and those that it
 // takes later are freed and loaded half a block apart, so the loads are spread
 // evenly and have a whole block's time (2048 cycles) to arrive at least.  8192^3:
-// 370 us, 2.97 PFLOP/s (`k_mul8_tile` with eight waves 428), the matrix unit
-// busy 70 % of the 1.9 to 2.1 GHz that random codes leave; with codes of 0, which
-// take less power, 288 us.
+// 380 to 400 us by the card, 2.8 PFLOP/s, the matrix unit busy 70 % of the 1.9 to
+// 2.1 GHz that random codes leave.  On a card where it took 370, `k_mul8_tile`
+// with eight waves took 428, and codes of 0, which take less power, 288.
 template <int FA, int FB>
 __global__ __launch_bounds__(256) void k_mul8_big(const Mul8Args a, const uint32_t tiles_m, const uint32_t tiles_n) {
     constexpr int BM = 256, BN = 256, L = 4;                 // loads of a wave for half a stage's A or B
@@ -848,6 +853,8 @@ hipError_t launch_kind(int kind, const Mul8Args& a, hipStream_t s) {
 // 256, 539 with 128 x 128, 921 with 64 x 64; fp32: 759, 842, 1380) and from tiles
 // that are alone: 777 x 1000 x 2048 in 7.5 and 14 us with 64 and 128 (fp32: 11, 18),
 // 1024 x 1024 x 8192 in fp32 in 33, 56 and 133, and with 128 in four parts in 29.
+// In between the table is short: 10.5 us for 2048^3 (16.6 measured), 15.8 for
+// 4096 x 4096 x 1024 (24.8), 6.9 for 64 x 4096 x 4096 (10.3), all in bf16.
 struct TileCost {
     int size, resident;
     double alone[2], full[2], fixed;   // [0]: bf16 and fp16, [1]: fp32
