@@ -118,3 +118,70 @@ def test_loads_into_lds_have_m0_to_themselves(tmp_path):
             assert all(body[i - 2].startswith("s_mov_b32 m0, ") for i in at), name
             assert sum("m0" in ins for ins in body) == len(at), name
     assert loads > 100
+
+
+def vectors(operands):
+    """Vector registers (file, number) in operands."""
+    found = set()
+    for file, low, high, one in re.findall(r"\b([va])(?:\[(\d+):(\d+)\]|(\d+)\b)", operands):
+        found |= {(file, k) for k in range(int(low or one), int(high or one) + 1)}
+    return found
+
+
+def split(operands):
+    return re.split(r",\s*(?![^\[]*\])", operands)
+
+
+def products_unready(body):
+    """What goes against hand-written matrix instructions whose hazards the
+    compiler does not see: an operand that a vector instruction wrote less than
+    two wait states before; an accumulator that anything else uses between the
+    first product and the last; results used before 48 wait states behind it."""
+    at = [i for i, ins in enumerate(body) if ins.startswith("v_mfma")]
+    sums, bad = set(), []
+    for i in at:
+        parts = split(body[i].partition(" ")[2])
+        sums |= vectors(parts[0])
+        states, used = 0, set().union(*(vectors(p) for p in parts[1:]))
+        for back in range(i - 1, -1, -1):
+            if states >= 2:
+                break
+            op, _, operands = body[back].partition(" ")
+            if op.startswith("v_") and not op.startswith("v_mfma") and vectors(split(operands)[0]) & used:
+                bad.append(f"{states} states: {body[back]} | {body[i]}")
+            wait = re.match(r"s_nop (0x[0-9a-f]+|\d+)", body[back])
+            states += int(wait.group(1), 0) + 1 if wait else 1
+    for ins in body[at[0]:at[-1]]:
+        if not ins.startswith("v_mfma") and vectors(ins.partition(" ")[2]) & sums:
+            bad.append(f"between the products: {ins}")
+    states = 0
+    for ins in body[at[-1] + 1:]:
+        if states >= 48:
+            break
+        if vectors(ins.partition(" ")[2]) & sums:
+            bad.append(f"{states} states behind the last product: {ins}")
+        wait = re.match(r"s_nop (0x[0-9a-f]+|\d+)", ins)
+        states += int(wait.group(1), 0) + 1 if wait else 1
+    return bad
+
+
+def test_the_scan_of_products_itself():
+    product = "v_mfma_scale_f32_16x16x128_f8f6f4 a[0:3], v[8:15], v[16:23], a[0:3], v1, v2 op_sel_hi:[0,0,0]"
+    wait = ["s_nop 15"] * 3
+    assert not products_unready(["v_accvgpr_write_b32 a0, 0", "s_nop 1", product] + wait + ["ds_write_b128 v5, a[0:3]"])
+    assert len(products_unready(["v_accvgpr_write_b32 a0, 0", "s_nop 0", product] + wait)) == 1
+    assert len(products_unready(["v_mov_b32_e32 v2, v3", product] + wait)) == 1
+    assert not products_unready(["v_mov_b32_e32 v3, v2", product] + wait)
+    assert len(products_unready([product, "v_accvgpr_read_b32 v4, a3", product] + wait)) == 1
+    assert len(products_unready([product] + wait[:2] + ["ds_write_b128 v5, a[0:3]"])) == 1
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
+def test_hand_written_products_wait(tmp_path):
+    seen = 0
+    for name, body in disassembled(tmp_path):
+        if "k_mul8_big" in name:
+            seen += 1
+            bad = products_unready(body)
+            assert not bad, f"{name}: {len(bad)}, e.g. {bad[0]}"
+    assert seen == 4
